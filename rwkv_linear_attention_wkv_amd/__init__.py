@@ -23,6 +23,7 @@ from . import _native
 from ._native import (WKV_ALGO_AUTO, WKV_ALGO_CHUNKED, WKV_ALGO_SCAN, WKV_DEV_BAD_LENGTH,  # noqa: F401
                       WKV_DEV_BAD_STATE_MAP, WKV_DEV_DUPLICATE_ROW,
                       WKV_DEV_TOKEN_OVERFLOW, WkvError, check)
+from ._marshal import _dev, _dtype_code, _out_code, _ptr, _same_dtype, _stream
 
 _lib = _native.load()
 
@@ -31,59 +32,15 @@ _ALGOS = {"auto": WKV_ALGO_AUTO, "scan": WKV_ALGO_SCAN, "chunked": WKV_ALGO_CHUN
 __all__ = ["wkv4_forward", "wkv5_forward", "wkv6_forward", "wkv6_forward_train", "wkv6_backward", "wkv6_forward_varlen", "varlen_plan", "VarlenPlan",
            "wkv7_forward", "wkv7_plan", "Wkv7Plan", "schedule_round_robin", "resolve_algo", "WkvError", "library"]
 
+from .ssm import *  # noqa: E402,F401,F403  (the state space operators)
+from .ssm import __all__ as _ssm_all  # noqa: E402
+
+__all__ += _ssm_all
+
 
 def library():
     """The loaded ctypes handle of libwkv.so."""
     return _lib
-
-
-def _dtype_code(t):
-    if t.dtype == torch.bfloat16:
-        return _native.WKV_BF16
-    if t.dtype == torch.float32:
-        return _native.WKV_F32
-    raise TypeError(f"unsupported input dtype {t.dtype} (bfloat16 or float32)")
-
-
-def _dev(t, name, dtype=None, shape=None):
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
-
-
-def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
-
-
-def _stream(ref):
-    return ctypes.c_void_p(torch.cuda.current_stream(ref.device).cuda_stream)
-
-
-def _out_code(y, out_dtype):
-    """Output dtype code: that of a given y, else out_dtype (float32 or bfloat16)."""
-    dt = y.dtype if y is not None else out_dtype
-    if dt == torch.float32:
-        return _native.WKV_F32, dt
-    if dt == torch.bfloat16:
-        return _native.WKV_BF16, dt
-    raise TypeError(f"unsupported output dtype {dt} (float32 or bfloat16)")
-
-
-def _same_dtype(name_tensors):
-    dts = {t.dtype for _, t in name_tensors if t is not None}
-    if len(dts) != 1:
-        raise TypeError("token inputs must share one dtype: " +
-                        ", ".join(f"{n}={t.dtype}" for n, t in name_tensors if t is not None))
 
 
 def wkv4_forward(time_decay, time_first, k, v, r=None, state=None, *, y=None, state_out=None,

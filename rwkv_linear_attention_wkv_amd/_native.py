@@ -11,6 +11,8 @@ WKV_OK, WKV_ERR_INVALID_ARG, WKV_ERR_UNSUPPORTED, WKV_ERR_DEVICE = 0, 1, 2, 3
 WKV_F32, WKV_BF16 = 0, 1
 WKV_ALGO_AUTO, WKV_ALGO_SCAN, WKV_ALGO_CHUNKED = 0, 1, 2
 WKV_LAYOUT_BTHN, WKV_LAYOUT_BHTN = 0, 1
+WKV_ACT_NONE, WKV_ACT_SILU = 0, 1
+WKV_STORE_INT8, WKV_STORE_E4M3 = 0, 1
 WKV_DEV_BAD_STATE_MAP = 1
 WKV_DEV_BAD_LENGTH = 2
 WKV_DEV_TOKEN_OVERFLOW = 4
@@ -53,6 +55,22 @@ SIGNATURES = {
     "wkv_abi_version": (_i, []),
 }
 
+# mirrors include/wkv_ssm.h
+_l = ctypes.c_int64
+_seq_dense = [_vp, _vp, _i, _vp, _vp, _vp]       # state_in, state_map, n_state, state_out, dev_status, stream
+_seq_slots = [_vp, _vp, _vp, _i, _vp, _vp]       # state_in, state_out, state_map, n_state, dev_status, stream
+_conv = [_vp, _l, _i, _vp, _vp, _i, _vp, _i]     # x, stride, dtype, weight, bias, act, y, out dtype
+_scan = [_vp, _l, _vp, _l, _vp, _vp, _l, _vp, _l, _i, _vp, _vp, _l, _vp, _i]  # x, dt, A, B, C, dtype, skip, z, dt_bias, softplus
+_store = [_vp, _vp, _i, _i, _vp, _i, _l, _vp, _vp, _i, _vp, _vp]
+SSM_SIGNATURES = {
+    "wkv_ssm_conv_forward": (_i, [_i] * 4 + _conv + _seq_dense),
+    "wkv_ssm_conv_forward_varlen": (_i, [_i] * 3 + [_vp, _i, _i] + _conv + _seq_slots),
+    "wkv_ssm_scan_forward": (_i, [_i] * 5 + _scan + [_vp, _i] + _seq_dense),
+    "wkv_ssm_scan_forward_varlen": (_i, [_i] * 4 + [_vp, _i, _i] + _scan + [_vp, _i] + _seq_slots),
+    "wkv_state_store_write": (_i, _store),
+    "wkv_state_store_read": (_i, _store),
+}
+
 _lib = None
 
 
@@ -72,7 +90,7 @@ def load(path: str = LIB_PATH):
             f"libwkv.so not found at {path}; build it with "
             "`python -m rwkv_linear_attention_wkv_amd.build` (hipcc, gfx950)")
     lib = ctypes.CDLL(path)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in {**SIGNATURES, **SSM_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -1,0 +1,86 @@
+// Host-side launchers of the state space kernels (internal to libwkv.so).
+// Arguments have been validated by the C ABI layer before these are called.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace wkv {
+
+// The sequences of a call and their state rows.  Dense: unit b holds tokens
+// [b*T, b*T + T), reads state row state_map[b] (or b, or the one shared row) and writes row b.
+// Varlen (lengths given): unit s holds lengths[s] packed tokens and reads and writes row
+// state_map[s] (or s).
+struct SeqParams {
+  int units;
+  int T;  // tokens of every row; varlen: the host's bound on every length
+  const int32_t *lengths;
+  long total_tokens;
+  const float *state_in;
+  const int32_t *state_map;
+  int n_state;
+  float *state_out;
+  int32_t *dev_status;
+};
+
+// A token array: element (token t of the call, column c) at base[t * stride + c].
+struct TokenArray {
+  const void *base;
+  long stride;
+};
+
+struct ConvParams {
+  SeqParams seq;
+  int D, W;
+  TokenArray x;
+  const float *weight, *bias;  // [D, W], [D] or null
+  bool silu;
+  void *y;  // [tokens, D], bf16 when y_bf16 (backward: dx)
+  bool y_bf16;
+  // backward
+  TokenArray dy;
+  bool dy_bf16;
+  const float *d_state_out;  // gradient of the final state, or null
+  float *d_state_in;         // or null
+  float *partial;            // [units * nseg, W + 1, D] sums of one segment: dweight taps, dbias
+  float *d_weight, *d_bias;
+  int seg_len, nseg;  // tokens of one workgroup's walk
+};
+
+hipError_t launch_ssm_conv(const ConvParams &p, bool bf16, hipStream_t s);
+hipError_t launch_ssm_conv_backward(const ConvParams &p, bool bf16, hipStream_t s);
+int conv_segments(int units, int T, int D, bool backward, int *seg_len);
+
+struct ScanSsmParams {
+  SeqParams seq;
+  int D, N, G;
+  TokenArray x, dt, z, Bm, Cm;  // z.base may be null
+  const float *A, *skip, *dt_bias;
+  bool softplus;
+  void *y;
+  bool y_bf16;
+  float *chunk_states;  // null, or [units, ceil(T/32) - 1, D, N]: the state at the start of chunks 1 ..
+};
+
+hipError_t launch_ssm_scan(const ScanSsmParams &p, bool bf16, hipStream_t s);
+
+// The 8-bit state store: rows of `row` values in groups of 64 with one scale each.
+struct StoreParams {
+  void *data;    // [n_store, row] codes
+  float *scale;  // [n_store, ceil(row / 64)]
+  float *states; // [n_state, row]
+  const int32_t *store_rows, *state_rows;  // [count] or null (identity)
+  int n_store, n_state, count;
+  long row;
+  bool e4m3;
+  int32_t *dev_status;
+};
+
+hipError_t launch_store_write(const StoreParams &p, hipStream_t s);
+hipError_t launch_store_read(const StoreParams &p, hipStream_t s);
+
+// out[c] = sum over r of in[r][c], rows in order within each of 16 strided parts.
+hipError_t launch_sum_rows(const float *in, float *out, long rows, long cols, hipStream_t s);
+
+}  // namespace wkv

@@ -1,0 +1,158 @@
+// The 8-bit store of carried states.  A row of `row` fp32 values is kept in groups of 64 (one key
+// row of a WKV head, a few channels of a scan state): scale = max|v| / 127 (int8) or / 448 (e4m3),
+// code = nearest to v / scale, ties to even; the last group may be short.  Both quotients are the
+// fp32 ones, correctly rounded, so that codes do not depend on the kernel.  A group of zeros has
+// scale 0; a group that holds an infinity or NaN has scale NaN and reads back as NaN throughout.
+//
+// Bound by memory (4 bytes in, 1 + 1/16 out, or the reverse): 16 lanes share a group, four values
+// each, so a wave reads 1 KiB in one load; the group's largest magnitude is four DPP steps.
+#include "ssm_device.hpp"
+
+namespace wkv {
+namespace {
+
+constexpr int kGroup = 64;
+
+// Whether item `item`'s destination row `to` is also another item's, for a whole wave.
+__device__ __forceinline__ bool shared_row(const int32_t *rows, int count, int item, int to, int lane) {
+  bool dup = false;
+  if (rows)
+    for (int i = lane; i < count; i += 64) dup |= i != item && rows[i] == to;
+  return __any(dup);
+}
+
+__device__ __forceinline__ bool store_item(const StoreParams &p, int item, int lane, bool to_store, long &cached, long &state) {
+  const int c = p.store_rows ? p.store_rows[item] : item, s = p.state_rows ? p.state_rows[item] : item;
+  int status = 0;
+  if (c < 0 || c >= p.n_store || s < 0 || s >= p.n_state) status |= WKV_DEV_BAD_STATE_MAP;
+  if (shared_row(to_store ? p.store_rows : p.state_rows, p.count, item, to_store ? c : s, lane)) status |= WKV_DEV_DUPLICATE_ROW;
+  if (status && lane == 0 && p.dev_status) atomicOr(p.dev_status, status);
+  cached = c;
+  state = s;
+  return status == 0;
+}
+
+template <bool E4M3, bool VEC>
+__global__ void __launch_bounds__(256) store_write_kernel(StoreParams p) {
+  const int lane = threadIdx.x & 63;
+  long cached, state;
+  if (!store_item(p, blockIdx.y, lane, true, cached, state)) return;
+  const long groups = (p.row + kGroup - 1) / kGroup;
+  const float *src = p.states + state * p.row;
+  uint8_t *dst = static_cast<uint8_t *>(p.data) + cached * p.row;
+  for (long g = (long)blockIdx.x * 16 + threadIdx.x / 16; g < (groups + 15) / 16 * 16; g += (long)gridDim.x * 16) {
+    const long e = g * kGroup + 4 * (threadIdx.x & 15);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (VEC) {
+      if (e < p.row) loadv<false>(src, e, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < p.row) v[i] = src[e + i];
+    }
+    // magnitudes compare as their bits do, with infinities and NaN above every number
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    const float limit = E4M3 ? 448.f : 127.f;
+    const bool finite = top < 0x7f800000u;
+    const float scale = finite ? __uint_as_float(top) / limit : __uint_as_float(0x7fc00000u);
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float r = scale > 0.f ? v[i] / scale : 0.f;
+      c[i] = fminf(fmaxf(r, -limit), limit);
+    }
+    uint32_t code;
+    if constexpr (E4M3) {
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+      code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    } else {
+      code = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) code |= ((uint32_t)(int)rintf(c[i]) & 0xffu) << (8 * i);
+    }
+    if constexpr (VEC) {
+      if (e < p.row) *reinterpret_cast<uint32_t *>(dst + e) = code;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < p.row) dst[e + i] = (uint8_t)(code >> (8 * i));
+    }
+    if ((threadIdx.x & 15) == 0 && g < groups) p.scale[cached * groups + g] = scale;
+  }
+}
+
+template <bool E4M3, bool VEC>
+__global__ void __launch_bounds__(256) store_read_kernel(StoreParams p) {
+  const int lane = threadIdx.x & 63;
+  long cached, state;
+  if (!store_item(p, blockIdx.y, lane, false, cached, state)) return;
+  const long groups = (p.row + kGroup - 1) / kGroup;
+  const uint8_t *src = static_cast<const uint8_t *>(p.data) + cached * p.row;
+  float *dst = p.states + state * p.row;
+  for (long g = (long)blockIdx.x * 16 + threadIdx.x / 16; g < groups; g += (long)gridDim.x * 16) {
+    const long e = g * kGroup + 4 * (threadIdx.x & 15);
+    const float scale = p.scale[cached * groups + g];
+    uint32_t code = 0;
+    if constexpr (VEC) {
+      if (e < p.row) code = *reinterpret_cast<const uint32_t *>(src + e);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < p.row) code |= (uint32_t)src[e + i] << (8 * i);
+    }
+    float v[4];
+    if constexpr (E4M3) {
+      v[0] = __builtin_amdgcn_cvt_f32_fp8((int)code, 0); v[1] = __builtin_amdgcn_cvt_f32_fp8((int)code, 1);
+      v[2] = __builtin_amdgcn_cvt_f32_fp8((int)code, 2); v[3] = __builtin_amdgcn_cvt_f32_fp8((int)code, 3);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(code >> (8 * i));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= scale;
+    if constexpr (VEC) {
+      if (e < p.row) storev<false>(dst, e, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < p.row) dst[e + i] = v[i];
+    }
+  }
+}
+
+dim3 store_grid(const StoreParams &p) {
+  const long blocks = ((p.row + kGroup - 1) / kGroup + 15) / 16;
+  return dim3((unsigned)(blocks < 4096 ? blocks : 4096), p.count);
+}
+
+}  // namespace
+
+hipError_t launch_store_write(const StoreParams &p, hipStream_t s) {
+  const bool vec = p.row % 4 == 0;  // the tables are 16-byte aligned
+  if (p.e4m3) {
+    if (vec) hipLaunchKernelGGL((store_write_kernel<true, true>), store_grid(p), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((store_write_kernel<true, false>), store_grid(p), dim3(256), 0, s, p);
+  } else {
+    if (vec) hipLaunchKernelGGL((store_write_kernel<false, true>), store_grid(p), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((store_write_kernel<false, false>), store_grid(p), dim3(256), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_store_read(const StoreParams &p, hipStream_t s) {
+  const bool vec = p.row % 4 == 0;
+  if (p.e4m3) {
+    if (vec) hipLaunchKernelGGL((store_read_kernel<true, true>), store_grid(p), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((store_read_kernel<true, false>), store_grid(p), dim3(256), 0, s, p);
+  } else {
+    if (vec) hipLaunchKernelGGL((store_read_kernel<false, true>), store_grid(p), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((store_read_kernel<false, false>), store_grid(p), dim3(256), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace wkv

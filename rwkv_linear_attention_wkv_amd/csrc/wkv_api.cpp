@@ -8,12 +8,15 @@
 #include <cstdio>
 #include <mutex>
 
+#include "api_common.hpp"
 #include "kernels.hpp"
 #include "wkv.h"
 
+namespace wkv {
+namespace api {
 namespace {
-
 thread_local char g_last_error[512] = "";
+}
 
 wkv_status fail(wkv_status s, const char *fmt, ...) {
   va_list ap;
@@ -28,24 +31,16 @@ wkv_status ok() {
   return WKV_OK;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace api
+}  // namespace wkv
 
-bool dtype_ok(wkv_dtype d) { return d == WKV_F32 || d == WKV_BF16; }
+using namespace wkv::api;
 
-wkv_status launched(hipError_t e, const char *what) {
-  if (e != hipSuccess) return fail(WKV_ERR_DEVICE, "%s: launch failed: %s", what, hipGetErrorString(e));
-  return ok();
-}
+namespace {
 
-constexpr int kMaxGridY = 65535;
 constexpr int kChunk = 64;
 // The chunked kernel addresses a chunk's token rows with 32-bit offsets.
 constexpr int kChunkedMaxRow = 1 << 23;
-
-#define REQUIRE(cond, ...)                                        \
-  do {                                                            \
-    if (!(cond)) return fail(WKV_ERR_INVALID_ARG, __VA_ARGS__);   \
-  } while (0)
 
 // Shared validation of the dense v5 / v6 calls.
 wkv_status check_dense56(const char *fn, int B, int T, int H, int N, const void *r, const void *k,

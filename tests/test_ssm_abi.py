@@ -1,0 +1,122 @@
+"""The state space operators on the CPU: exported symbols, host validation of the C ABI and of the binding.  Nothing
+here launches a kernel: every call fails validation, which comes before any HIP call, or has nothing to do."""
+import os
+import re
+
+import pytest
+import torch
+
+import rwkv_linear_attention_wkv_amd as wkv
+from rwkv_linear_attention_wkv_amd import _native as nat
+from rwkv_linear_attention_wkv_amd import ssm
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P, MIS, ODD = 0x10000, 0x10002, 0x10001  # never dereferenced
+E, U, OK = nat.WKV_ERR_INVALID_ARG, nat.WKV_ERR_UNSUPPORTED, nat.WKV_OK
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return nat.load()
+
+
+def test_exports_every_declared_symbol(lib):
+    text = open(os.path.join(ROOT, "include", "wkv_ssm.h")).read()
+    names = re.findall(r"WKV_API\s+[\w\s\*]+?\b(\w+)\s*\(", text)
+    assert set(names) == set(nat.SSM_SIGNATURES) and len(names) == len(set(names))
+    for name in names:
+        assert hasattr(lib, name), name
+
+
+def conv(lib, B=2, T=8, D=64, W=4, x=P, xs=64, dt=1, w=P, b=P, act=1, y=2 * P, od=0, si=None, sm=None, ns=0, so=None, ds=None):
+    return lib.wkv_ssm_conv_forward(B, T, D, W, x, xs, dt, w, b, act, y, od, si, sm, ns, so, ds, None)
+
+
+def conv_slots(lib, S=2, D=64, W=4, ln=P, ml=8, tt=16, x=P, xs=64, dt=1, w=P, b=P, act=1, y=2 * P, od=0, si=P, so=P, sm=None, ns=2, ds=None):
+    return lib.wkv_ssm_conv_forward_varlen(S, D, W, ln, ml, tt, x, xs, dt, w, b, act, y, od, si, so, sm, ns, ds, None)
+
+
+def scan(lib, B=2, T=8, D=64, N=16, G=1, x=P, xs=64, d=P, dst=64, A=P, b=P, bs=16, c=P, cs=16, dt=1, sk=P, z=P, zs=64, db=P, sp=1,
+         y=2 * P, od=0, si=None, sm=None, ns=0, so=None, ds=None):
+    return lib.wkv_ssm_scan_forward(B, T, D, N, G, x, xs, d, dst, A, b, bs, c, cs, dt, sk, z, zs, db, sp, y, od, si, sm, ns, so, ds, None)
+
+
+def scan_slots(lib, S=2, D=64, N=16, G=1, ln=P, ml=8, tt=16, x=P, xs=64, d=P, dst=64, A=P, b=P, bs=16, c=P, cs=16, dt=1, sk=P, z=P,
+               zs=64, db=P, sp=1, y=2 * P, od=0, si=P, so=P, sm=None, ns=2, ds=None):
+    return lib.wkv_ssm_scan_forward_varlen(S, D, N, G, ln, ml, tt, x, xs, d, dst, A, b, bs, c, cs, dt, sk, z, zs, db, sp, y, od, si,
+                                           so, sm, ns, ds, None)
+
+
+@pytest.mark.parametrize("fn", [conv, scan])
+def test_dense_refusals(lib, fn):
+    for kw in (dict(B=0), dict(T=-1), dict(B=70000), dict(D=0), dict(D=1 << 25), dict(x=None), dict(x=ODD), dict(xs=63),
+               dict(y=None), dict(y=0x10008), dict(y=P), dict(si=0x10008, ns=1), dict(si=P, ns=0), dict(si=P, ns=3), dict(sm=P),
+               dict(si=P, sm=MIS, ns=3), dict(si=P, so=P, ns=1), dict(si=P, so=P, sm=P, ns=2), dict(so=0x10008), dict(ds=MIS)):
+        assert fn(lib, **kw) == E, kw
+        assert lib.wkv_last_error()
+    assert fn(lib, dt=5) == U and fn(lib, od=5) == U
+    assert fn(lib, T=0) == OK  # no tokens and no state to hand on
+
+
+@pytest.mark.parametrize("fn", [conv_slots, scan_slots])
+def test_varlen_refusals(lib, fn):
+    for kw in (dict(S=-1), dict(S=70000), dict(ml=-1), dict(tt=-1), dict(ln=None), dict(ln=MIS), dict(si=None), dict(so=None),
+               dict(si=0x10008), dict(ns=0), dict(ns=1), dict(sm=MIS), dict(x=None), dict(y=None), dict(ds=MIS)):
+        assert fn(lib, **kw) == E, kw
+    assert fn(lib, S=0) == OK
+
+
+def test_conv_refusals(lib):
+    for W in (0, 1, 5):
+        assert conv(lib, W=W) == U
+    assert conv(lib, act=2) == U
+    assert conv(lib, w=None) == E and conv(lib, w=MIS) == E and conv(lib, b=MIS) == E
+
+
+def test_scan_refusals(lib):
+    assert scan(lib, N=0) == U and scan(lib, N=65, bs=65, cs=65) == U
+    for kw in (dict(G=0), dict(G=3), dict(A=None), dict(A=0x10008), dict(d=None), dict(b=None), dict(c=None), dict(dst=10),
+               dict(bs=15), dict(cs=15), dict(G=2, bs=16), dict(zs=10), dict(sk=MIS), dict(db=MIS), dict(z=ODD), dict(d=2 * P), dict(z=2 * P)):
+        assert scan(lib, **kw) == E, kw
+
+
+def store(fn, data=P, scale=P, n=4, fmt=0, st=P, ns=4, row=64, sr=None, tr=None, count=4, ds=None):
+    return fn(data, scale, n, fmt, st, ns, row, sr, tr, count, ds, None)
+
+
+@pytest.mark.parametrize("name", ["wkv_state_store_write", "wkv_state_store_read"])
+def test_store_refusals(lib, name):
+    fn = getattr(lib, name)
+    for kw in (dict(count=-1), dict(n=-1), dict(ns=-1), dict(row=0), dict(count=70000, sr=P, tr=P), dict(data=None), dict(scale=None),
+               dict(st=None), dict(data=0x10008), dict(st=0x10008), dict(scale=MIS), dict(n=3), dict(ns=3), dict(sr=MIS), dict(tr=MIS),
+               dict(ds=MIS)):
+        assert store(fn, **kw) == E, kw
+    assert store(fn, fmt=2) == U
+    assert store(fn, count=0) == OK
+
+
+def test_row_steps_of_views():
+    """The step between the rows of token arrays, and the views that have none."""
+    t = torch.zeros(3, 5, 40)
+    step = lambda v, inner: ssm._rows(v, "x", v.shape[:v.dim() - len(inner)], inner, v)[1]  # noqa: E731
+    assert step(t, (40,)) == 40 and step(t[..., 8:24], (16,)) == 40 and step(t[:, :, ::40], (1,)) == 40
+    assert step(t[:1, 1:4, :8], (8,)) == 40 and step(t[:, :1, :8], (8,)) == 200 and step(t[0, :, 4:9], (5,)) == 40
+    assert step(t[:1, :1, :8], (8,)) == 8 and step(t[..., :12].unflatten(-1, (3, 4)), (3, 4)) == 40
+    for bad, inner in ((t[:, :3], (40,)), (t[..., ::2], (20,)), (t.transpose(0, 1), (40,)), (t[:, :1].expand(3, 5, 40), (40,)),
+                       (t.unflatten(-1, (5, 8))[..., :4], (5, 4))):
+        with pytest.raises(ValueError):
+            step(bad, inner)
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    x = torch.zeros(2, 3, 8)
+    with pytest.raises(ValueError, match="device tensor"):
+        wkv.ssm_conv_forward(x, torch.zeros(8, 4))
+    with pytest.raises(ValueError, match="dimensions"):
+        wkv.ssm_conv_forward(x[0], torch.zeros(8, 4))
+    with pytest.raises(TypeError, match="dtype"):
+        wkv.ssm_scan_forward(x.half(), x, torch.zeros(8, 4), x, x)
+    with pytest.raises(TypeError, match="store format"):
+        wkv.state_store_alloc(1, 64, format=torch.uint8, device="cpu")
+    with pytest.raises(TypeError, match="store format"):
+        wkv.state_store_write(torch.zeros(2, 64), torch.zeros(2, 1), torch.zeros(2, 64))
