@@ -69,6 +69,11 @@ WKV_API wkv_status wkv_ssm_conv_forward_varlen(int num_slots, int D, int W,
                         const float *state_in, float *state_out, const int32_t *state_map,
                         int n_state, int32_t *dev_status, void *stream);
 
+/* Bytes of workspace with which a scan of `rows` sequences (batch rows or
+ * slots) of up to T tokens is cut into segments that run side by side: 0 where
+ * the rows alone fill the chip, and for T <= 64.  Pure host function. */
+WKV_API size_t wkv_ssm_scan_workspace(int rows, int T, int D, int N, int G);
+
 /*
  * Selective scan.  D channels in G equal groups that share B and C; state
  * h[d][n] of N = 1 .. 64 values per channel:
@@ -83,6 +88,10 @@ WKV_API wkv_status wkv_ssm_conv_forward_varlen(int num_slots, int D, int W,
  *   y          [B,T,D] out_dtype
  *   state_in   [n_state,D,N] fp32 or NULL (zeros); state_map, n_state, state_out
  *              ([B,D,N]), dev_status as wkv_ssm_conv_forward
+ *   workspace  16-byte aligned device memory of at least
+ *              wkv_ssm_scan_workspace(B, T, D, N, G) bytes, whose content does not
+ *              matter and which no other call may use until this one is done; NULL:
+ *              the sequences are not cut (slower where they are few and long)
  * A token whose delta is 0 (dt = -inf under the softplus) leaves the state as
  * it is, so rows may be padded on either side that way.
  */
@@ -93,7 +102,8 @@ WKV_API wkv_status wkv_ssm_scan_forward(int B, int T, int D, int N, int G,
                         const float *skip, const void *z, int64_t z_stride,
                         const float *dt_bias, int dt_softplus, void *y, wkv_dtype out_dtype,
                         const float *state_in, const int32_t *state_map, int n_state,
-                        float *state_out, int32_t *dev_status, void *stream);
+                        float *state_out, void *workspace, size_t workspace_bytes,
+                        int32_t *dev_status, void *stream);
 
 /* The same for slots: token arrays are packed [total_tokens, ..]; slot s reads
  * and writes state row state_map[s] (NULL: s) of [n_state,D,N]. */
@@ -105,7 +115,8 @@ WKV_API wkv_status wkv_ssm_scan_forward_varlen(int num_slots, int D, int N, int 
                         const float *skip, const void *z, int64_t z_stride,
                         const float *dt_bias, int dt_softplus, void *y, wkv_dtype out_dtype,
                         const float *state_in, float *state_out, const int32_t *state_map,
-                        int n_state, int32_t *dev_status, void *stream);
+                        int n_state, void *workspace, size_t workspace_bytes,
+                        int32_t *dev_status, void *stream);
 
 /*
  * 8-bit store of carried states (snapshots of a prefix, parked slots): rows of

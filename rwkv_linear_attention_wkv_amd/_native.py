@@ -65,8 +65,9 @@ _store = [_vp, _vp, _i, _i, _vp, _i, _l, _vp, _vp, _i, _vp, _vp]
 SSM_SIGNATURES = {
     "wkv_ssm_conv_forward": (_i, [_i] * 4 + _conv + _seq_dense),
     "wkv_ssm_conv_forward_varlen": (_i, [_i] * 3 + [_vp, _i, _i] + _conv + _seq_slots),
-    "wkv_ssm_scan_forward": (_i, [_i] * 5 + _scan + [_vp, _i] + _seq_dense),
-    "wkv_ssm_scan_forward_varlen": (_i, [_i] * 4 + [_vp, _i, _i] + _scan + [_vp, _i] + _seq_slots),
+    "wkv_ssm_scan_workspace": (ctypes.c_size_t, [_i] * 5),
+    "wkv_ssm_scan_forward": (_i, [_i] * 5 + _scan + [_vp, _i] + _seq_dense[:4] + [_vp, ctypes.c_size_t, _vp, _vp]),
+    "wkv_ssm_scan_forward_varlen": (_i, [_i] * 4 + [_vp, _i, _i] + _scan + [_vp, _i] + _seq_slots[:4] + [_vp, ctypes.c_size_t, _vp, _vp]),
     "wkv_state_store_write": (_i, _store),
     "wkv_state_store_read": (_i, _store),
 }

@@ -60,9 +60,21 @@ struct ScanSsmParams {
   bool softplus;
   void *y;
   bool y_bf16;
-  float *chunk_states;  // null, or [units, ceil(T/32) - 1, D, N]: the state at the start of chunks 1 ..
+  // null, or [units, n_chunks, D, N]: the state at the start of each 32-token chunk but the first
+  float *chunk_states;
+  int n_chunks;
+  int seg_len, nseg;  // tokens of a segment; with nseg > 1 the workspace holds the segments' states
+  float *workspace;   // [units][nseg][D][N] states, [units][nseg - 1][D] sums of delta
 };
 
+constexpr int kScanChunk = 32;  // tokens between saved states
+constexpr int kScanShort = 8;   // calls of at most this many tokens a sequence take the kernel without tiles
+constexpr int kScanSplit = 64;  // a segment is a multiple of this; no shorter sequence is split
+
+// Lanes that share a channel, four states each.
+inline int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+
+int scan_segments(int units, int T, int D, int N, int G, int *seg_len);
 hipError_t launch_ssm_scan(const ScanSsmParams &p, bool bf16, hipStream_t s);
 
 // The 8-bit state store: rows of `row` values in groups of 64 with one scale each.

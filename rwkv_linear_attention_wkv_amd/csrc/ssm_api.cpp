@@ -104,6 +104,10 @@ wkv_status conv(const char *fn, const wkv::SeqParams &seq, int D, int W, const v
   return launched(wkv::launch_ssm_conv(p, in_dtype == WKV_BF16, static_cast<hipStream_t>(stream)), fn);
 }
 
+size_t scan_workspace(int units, int nseg, int D, int N) {
+  return nseg > 1 ? sizeof(float) * (size_t)units * ((size_t)nseg * D * N + (size_t)(nseg - 1) * D) : 0;
+}
+
 // Checks shared by the scan's calls, and their parameters.
 wkv_status scan_params(const char *fn, const wkv::SeqParams &seq, int D, int N, int G, const void *x,
                        int64_t x_stride, const void *dt, int64_t dt_stride, const float *A, const void *Bm,
@@ -135,7 +139,7 @@ wkv_status scan_params(const char *fn, const wkv::SeqParams &seq, int D, int N, 
 }
 
 wkv_status scan(const char *fn, wkv::ScanSsmParams &p, wkv_dtype in_dtype, void *y, wkv_dtype out_dtype,
-                void *stream) {
+                void *workspace, size_t workspace_bytes, void *stream) {
   if (!dtype_ok(out_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, out_dtype);
   if (p.seq.units == 0) return ok();
   if (p.seq.total_tokens > 0) {
@@ -145,6 +149,17 @@ wkv_status scan(const char *fn, wkv::ScanSsmParams &p, wkv_dtype in_dtype, void 
     return ok();
   }
   p.y = y; p.y_bf16 = out_dtype == WKV_BF16;
+  p.nseg = wkv::scan_segments(p.seq.units, p.seq.T, p.D, p.N, p.G, &p.seg_len);
+  if (p.nseg > 1) {
+    const size_t need = scan_workspace(p.seq.units, p.nseg, p.D, p.N);
+    if (workspace) {
+      REQUIRE(aligned(workspace, 16) && workspace_bytes >= need,
+              "%s: the workspace must be 16-byte aligned and hold %zu bytes (got %zu)", fn, need, workspace_bytes);
+      p.workspace = static_cast<float *>(workspace);
+    } else {
+      p.nseg = 1; p.seg_len = p.seq.T;  // every sequence in one piece
+    }
+  }
   return launched(wkv::launch_ssm_scan(p, in_dtype == WKV_BF16, static_cast<hipStream_t>(stream)), fn);
 }
 
@@ -195,19 +210,26 @@ wkv_status wkv_ssm_conv_forward_varlen(int num_slots, int D, int W, const int32_
   return conv(fn, seq, D, W, x, x_stride, in_dtype, weight, bias, act, y, out_dtype, stream);
 }
 
+size_t wkv_ssm_scan_workspace(int rows, int T, int D, int N, int G) {
+  if (rows < 1 || T < 1 || D < 1 || N < 1 || N > kMaxStates || G < 1 || D % G) return 0;
+  int len;
+  return scan_workspace(rows, wkv::scan_segments(rows, T, D, N, G, &len), D, N);
+}
+
 wkv_status wkv_ssm_scan_forward(int B, int T, int D, int N, int G, const void *x, int64_t x_stride, const void *dt,
                                 int64_t dt_stride, const float *A, const void *Bm, int64_t b_stride, const void *Cm,
                                 int64_t c_stride, wkv_dtype in_dtype, const float *skip, const void *z,
                                 int64_t z_stride, const float *dt_bias, int dt_softplus, void *y,
                                 wkv_dtype out_dtype, const float *state_in, const int32_t *state_map, int n_state,
-                                float *state_out, int32_t *dev_status, void *stream) {
+                                float *state_out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                void *stream) {
   const char *fn = "wkv_ssm_scan_forward";
   wkv::SeqParams seq;
   CHECK(dense_seq(fn, B, T, state_in, state_map, n_state, state_out, dev_status, &seq));
   wkv::ScanSsmParams p;
   CHECK(scan_params(fn, seq, D, N, G, x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, in_dtype, skip, z,
                     z_stride, dt_bias, dt_softplus, &p));
-  return scan(fn, p, in_dtype, y, out_dtype, stream);
+  return scan(fn, p, in_dtype, y, out_dtype, workspace, workspace_bytes, stream);
 }
 
 wkv_status wkv_ssm_scan_forward_varlen(int num_slots, int D, int N, int G, const int32_t *lengths, int max_len,
@@ -216,14 +238,15 @@ wkv_status wkv_ssm_scan_forward_varlen(int num_slots, int D, int N, int G, const
                                        const void *Cm, int64_t c_stride, wkv_dtype in_dtype, const float *skip,
                                        const void *z, int64_t z_stride, const float *dt_bias, int dt_softplus,
                                        void *y, wkv_dtype out_dtype, const float *state_in, float *state_out,
-                                       const int32_t *state_map, int n_state, int32_t *dev_status, void *stream) {
+                                       const int32_t *state_map, int n_state, void *workspace,
+                                       size_t workspace_bytes, int32_t *dev_status, void *stream) {
   const char *fn = "wkv_ssm_scan_forward_varlen";
   wkv::SeqParams seq;
   CHECK(varlen_seq(fn, num_slots, lengths, max_len, total_tokens, state_in, state_out, state_map, n_state, dev_status, &seq));
   wkv::ScanSsmParams p;
   CHECK(scan_params(fn, seq, D, N, G, x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, in_dtype, skip, z,
                     z_stride, dt_bias, dt_softplus, &p));
-  return scan(fn, p, in_dtype, y, out_dtype, stream);
+  return scan(fn, p, in_dtype, y, out_dtype, workspace, workspace_bytes, stream);
 }
 
 wkv_status wkv_state_store_write(void *data, float *scale, int n_store, wkv_store_format format,

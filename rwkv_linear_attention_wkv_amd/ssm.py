@@ -208,6 +208,12 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code):
                          _flat(dt_bias, "dt_bias", torch.float32, torch.Size((width,)), x), int(bool(dt_softplus)))
 
 
+def _workspace(rows, T, width, N, G, ref):
+    """Memory for a scan that is cut into segments, allocated on the current stream for one call, or None; its bytes."""
+    need = _lib.wkv_ssm_scan_workspace(rows, T, width, N, G) if T > 64 else 0
+    return (torch.empty(need // 4, dtype=torch.float32, device=ref.device) if need else None), need
+
+
 def ssm_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, state_map=None, *, dt_softplus=True,
                      y=None, state_out=None, return_state=True, dev_status=None, out_dtype=torch.float32):
     """Selective state space scan.
@@ -224,7 +230,9 @@ def ssm_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, s
     width, N, G, args = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code)
     states, state_out = _dense_states(state, state_map, state_out, return_state, rows, (width, N), x)
     y, oc = _output(y, out_dtype, x.shape, x)
-    _launch(x, _lib.wkv_ssm_scan_forward, rows, T, width, N, G, *args, y.data_ptr(), oc, *states, _status(dev_status, x))
+    ws, ws_bytes = _workspace(rows, T, width, N, G, x)
+    _launch(x, _lib.wkv_ssm_scan_forward, rows, T, width, N, G, *args, y.data_ptr(), oc, *states, _ptr(ws), ws_bytes,
+            _status(dev_status, x))
     return y, state_out
 
 
@@ -240,8 +248,9 @@ def ssm_scan_forward_varlen(lengths, x, dt, A, B, C, state, *, max_len, D=None, 
     width, N, G, args = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code)
     S, ln, states = _slot_states(lengths, state, state_map, state_out, (width, N), x)
     y, oc = _output(y, out_dtype, x.shape, x)
+    ws, ws_bytes = _workspace(S, int(max_len), width, N, G, x)
     _launch(x, _lib.wkv_ssm_scan_forward_varlen, S, width, N, G, ln, int(max_len), total, *args, y.data_ptr(), oc,
-            *states, _status(dev_status, x))
+            *states, _ptr(ws), ws_bytes, _status(dev_status, x))
     return y
 
 

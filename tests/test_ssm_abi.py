@@ -37,14 +37,14 @@ def conv_slots(lib, S=2, D=64, W=4, ln=P, ml=8, tt=16, x=P, xs=64, dt=1, w=P, b=
 
 
 def scan(lib, B=2, T=8, D=64, N=16, G=1, x=P, xs=64, d=P, dst=64, A=P, b=P, bs=16, c=P, cs=16, dt=1, sk=P, z=P, zs=64, db=P, sp=1,
-         y=2 * P, od=0, si=None, sm=None, ns=0, so=None, ds=None):
-    return lib.wkv_ssm_scan_forward(B, T, D, N, G, x, xs, d, dst, A, b, bs, c, cs, dt, sk, z, zs, db, sp, y, od, si, sm, ns, so, ds, None)
+         y=2 * P, od=0, si=None, sm=None, ns=0, so=None, ws=None, wb=0, ds=None):
+    return lib.wkv_ssm_scan_forward(B, T, D, N, G, x, xs, d, dst, A, b, bs, c, cs, dt, sk, z, zs, db, sp, y, od, si, sm, ns, so, ws, wb, ds, None)
 
 
 def scan_slots(lib, S=2, D=64, N=16, G=1, ln=P, ml=8, tt=16, x=P, xs=64, d=P, dst=64, A=P, b=P, bs=16, c=P, cs=16, dt=1, sk=P, z=P,
-               zs=64, db=P, sp=1, y=2 * P, od=0, si=P, so=P, sm=None, ns=2, ds=None):
+               zs=64, db=P, sp=1, y=2 * P, od=0, si=P, so=P, sm=None, ns=2, ws=None, wb=0, ds=None):
     return lib.wkv_ssm_scan_forward_varlen(S, D, N, G, ln, ml, tt, x, xs, d, dst, A, b, bs, c, cs, dt, sk, z, zs, db, sp, y, od, si,
-                                           so, sm, ns, ds, None)
+                                           so, sm, ns, ws, wb, ds, None)
 
 
 @pytest.mark.parametrize("fn", [conv, scan])
@@ -78,6 +78,15 @@ def test_scan_refusals(lib):
     for kw in (dict(G=0), dict(G=3), dict(A=None), dict(A=0x10008), dict(d=None), dict(b=None), dict(c=None), dict(dst=10),
                dict(bs=15), dict(cs=15), dict(G=2, bs=16), dict(zs=10), dict(sk=MIS), dict(db=MIS), dict(z=ODD), dict(d=2 * P), dict(z=2 * P)):
         assert scan(lib, **kw) == E, kw
+
+
+def test_scan_workspace(lib):
+    need = lib.wkv_ssm_scan_workspace(1, 4096, 64, 16, 1)
+    assert need > 0 and lib.wkv_ssm_scan_workspace(1, 64, 64, 16, 1) == 0 and lib.wkv_ssm_scan_workspace(64, 4096, 4096, 16, 1) == 0
+    for bad in ((0, 4096, 64, 16, 1), (1, 4096, 64, 0, 1), (1, 4096, 64, 65, 1), (1, 4096, 64, 16, 3), (1, -1, 64, 16, 1)):
+        assert lib.wkv_ssm_scan_workspace(*bad) == 0
+    assert scan(lib, B=1, T=4096, ws=P, wb=need - 1) == E and b"workspace" in lib.wkv_last_error()
+    assert scan(lib, B=1, T=4096, ws=0x10008, wb=need) == E
 
 
 def store(fn, data=P, scale=P, n=4, fmt=0, st=P, ns=4, row=64, sr=None, tr=None, count=4, ds=None):

@@ -248,6 +248,29 @@ def test_scan_in_place_state_and_carry(T):
     check_scan(c, c["state"], torch.cat(ys, 1), st, F32)
 
 
+@pytest.mark.parametrize("T,D,N,dtype", [(1025, 70, 16, F32), (777, 300, 7, BF16), (641, 24, 48, F32), (700, 40, 32, F32), (2000, 9, 3, F32)])
+def test_scan_one_long_row(T, D, N, dtype):
+    """A row that is cut into segments, with and without a workspace, and as a slot next to short ones."""
+    c = scan_case(1, T, D, N, 0, dtype)
+    assert wkv.library().wkv_ssm_scan_workspace(1, T, D, N, 1) > 0
+    st = gpu(c["state"])
+    y, last = run_scan(c, st, state_out=st)
+    check_scan(c, c["state"], y, last, F32)
+    lengths = [0, 3, T, 1]
+    first = draw(50, 4, D, N)
+    first[2] = c["state"][0]
+    flat = {k: torch.cat([draw(51, 3, *c[k].shape[2:], dtype=dtype), c[k][0], draw(52, 1, *c[k].shape[2:], dtype=dtype)])
+            for k in ("x", "dt", "B", "C", "z")}
+    st = gpu(first)
+    yv = wkv.ssm_scan_forward_varlen(gpu(torch.tensor(lengths, dtype=torch.int32)), *(gpu(flat[k]) for k in ("x", "dt")), gpu(c["A"]),
+                                     gpu(flat["B"]), gpu(flat["C"]), st, max_len=T + 9, D=gpu(c["D"]), z=gpu(flat["z"]),
+                                     dt_bias=gpu(c["dt_bias"]))
+    assert torch.equal(st[0].cpu(), first[0])
+    check_scan(c, c["state"], yv[None, 3:T + 3], st[2:3], F32)
+    short = {**c, **{k: v[None, :3] for k, v in flat.items()}}
+    check_scan(short, first[1:2], yv[None, :3], st[1:2], F32)
+
+
 def test_scan_state_map_and_shared_state():
     c = scan_case(3, 12, 40, 16, 0, F32, n_state=5)
     rows = torch.tensor([4, 0, 4], dtype=torch.int32)
