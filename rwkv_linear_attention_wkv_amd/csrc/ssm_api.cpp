@@ -65,7 +65,7 @@ wkv_status token_array(const char *fn, const char *name, const void *base, int64
                        wkv_dtype dtype) {
   REQUIRE(base, "%s: %s must be non-NULL", fn, name);
   REQUIRE(aligned(base, dtype == WKV_BF16 ? 2 : 4), "%s: %s must be aligned to its element", fn, name);
-  REQUIRE(stride >= width && stride <= ((int64_t)1 << 31), "%s: %s has row stride %lld for rows of %ld", fn, name,
+  REQUIRE(stride >= width && stride <= wkv::kMaxStride, "%s: %s has row stride %lld for rows of %ld", fn, name,
           (long long)stride, width);
   return WKV_OK;
 }

@@ -145,6 +145,18 @@ __device__ __forceinline__ float softplus_f(float v) {
   return fmaxf(v, 0.f) + 2.f * s * r;
 }
 
+// A window of a token array for buffer loads and stores: `rows` rows from `row` on, columns from c
+// on.  Accesses past its last row read 0 and write nothing; columns that a lane does not have are
+// sent there by adding kOutside to their offset.  Offsets are 32-bit: at most 32 rows, of row strides
+// up to kMaxStride.
+constexpr uint32_t kOutside = 0x80000000u;
+template <int ELEM>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void *base, long stride, long row, int rows, long c, int cols) {
+  const char *at = static_cast<const char *>(base) + (row * stride + c) * ELEM;
+  const uint32_t n = rows > 0 ? (uint32_t)(((rows - 1) * stride + cols) * ELEM) : 0u;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), 0, (int)n, 0x00020000);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The value of the lane that DPP control CTRL selects (every lane of the row is active).

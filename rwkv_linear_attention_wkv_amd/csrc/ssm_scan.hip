@@ -75,51 +75,78 @@ __global__ void __launch_bounds__(256) ssm_scan_short_kernel(ScanSsmParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Long sequences.  A workgroup of four waves owns 256 / LN channels and walks its segment in tiles
-// of TT tokens.  Per tile, all threads first load (coalesced rows, one tile ahead) and form what a
-// token and channel need once - delta, delta x - and the widened B and C rows, into LDS; then LN
-// adjacent lanes walk a channel's tokens with four states each in registers; their partial sums over
-// n are spread over the LN lanes by DPP halvings (LN tokens at a time), go back through LDS, and are
-// finished (skip, gate, rounding) in the loading threads' layout, for row-wide stores.  Both LDS
-// sides are double-buffered: one barrier per tile.
+// Long sequences.  A workgroup owns 256 / LN channels and walks its segment in tiles of TT tokens,
+// with four waves for each of two roles and one barrier per tile:
+//   - the staging waves load a tile's rows (one tile ahead), form what a token and channel need once
+//     - delta, delta x - and the widened B and C rows into LDS, and finish the results of the tile
+//     before (skip, gate, rounding) for row-wide stores;
+//   - the scan waves walk the channels: four states of a channel per lane, LN lanes a channel.  The
+//     matrix unit adds the outer product: v_mfma_f32_4x4x1 takes, per block of four lanes, four B
+//     values and four delta x and adds their product to the 4 x 4 decayed states, so that a state
+//     costs a lane two multiplies, an exponential and the multiply-add into y.  (fp32 throughout.)
+//     The partial sums over n are spread over the LN lanes, LN tokens at a time.
 //
 // Few rows: the sequence is cut into nseg segments.  The carry pass runs all but the last from a
 // state of zero and leaves each one's final state and its sum of delta; as the decay over a segment
 // is e^(A sum delta), the main pass folds the earlier segments' states into its own start.
 
+// VW adjacent elements as loaded: widened when they are used, so that no load is waited for early.
 template <bool BF16, bool VEC, int VW>
-struct RawRow {  // VW adjacent elements as loaded
+struct RawRow {
   uint32_t w[VEC && BF16 ? (VW + 1) / 2 : VW];
-  __device__ __forceinline__ void load(const TokenArray &a, long row, long c, int live) {
-#pragma unroll
-    for (auto &x : w) x = 0;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, const uint32_t (&col)[VEC ? 1 : VW]) {
     if constexpr (VEC) {
-      if (live > 0) {
-        const char *at = static_cast<const char *>(a.base) + (row * a.stride + c) * (BF16 ? 2 : 4);
-        if constexpr (sizeof w == 16) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(at);
-          w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-        } else if constexpr (sizeof w == 8) {
-          const uint2 v = *reinterpret_cast<const uint2 *>(at);
-          w[0] = v.x; w[1] = v.y;
-        } else {
-          w[0] = *reinterpret_cast<const uint32_t *>(at);
-        }
+      if constexpr (sizeof w == 16) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(row + col[0]), 0, 0);
+        w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
+      } else if constexpr (sizeof w == 8) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)(row + col[0]), 0, 0);
+        w[0] = v[0]; w[1] = v[1];
+      } else {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)(row + col[0]), 0, 0);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (e < live) {
-          if constexpr (BF16) w[e] = (uint32_t) static_cast<const uint16_t *>(a.base)[row * a.stride + c + e] << 16;
-          else w[e] = static_cast<const uint32_t *>(a.base)[row * a.stride + c + e];
-        }
+      for (int e = 0; e < VW; ++e) {
+        if constexpr (BF16) w[e] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)(row + col[e]), 0, 0);
+        else w[e] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)(row + col[e]), 0, 0);
+      }
     }
+  }
+  // Keeps every use behind this point, so that the wait for the loads stays there.
+  __device__ __forceinline__ void arrive() {
+#pragma unroll
+    for (auto &x : w) asm volatile("" : "+v"(x));
   }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (VEC && BF16) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    else if constexpr (BF16) return bf16_lo(w[e]);
     else return __uint_as_float(w[e]);
   }
 };
+
+// VW adjacent results through a window.
+template <bool BF16, bool VEC, int VW>
+__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t row, const uint32_t (&col)[VEC ? 1 : VW], const float (&v)[VW]) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      if constexpr (BF16) __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(v[e]), r, (int)(row + col[e]), 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), r, (int)(row + col[e]), 0, 0);
+    }
+  } else if constexpr (BF16) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    if constexpr (VW == 4) __builtin_amdgcn_raw_buffer_store_b64(u2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, r, (int)(row + col[0]), 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(v[0], v[1]), r, (int)(row + col[0]), 0, 0);
+  } else {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    if constexpr (VW == 4)
+      __builtin_amdgcn_raw_buffer_store_b128(u4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, r,
+                                             (int)(row + col[0]), 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b64(u2{__float_as_uint(v[0]), __float_as_uint(v[1])}, r, (int)(row + col[0]), 0, 0);
+  }
+}
 
 template <int LN>
 struct Tile {
@@ -129,19 +156,73 @@ struct Tile {
   static constexpr int VW = PT < 4 ? PT : 4;          // of them adjacent channels
   static constexpr int NI = PT / VW;
   static constexpr int NP = 4 * LN;                   // states of a channel, padded
-  static constexpr int NBC = (TT * 2 * NP + 255) / 256;  // B and C values that a thread loads
+  static constexpr int NB = (TT * NP + 255) / 256;    // B (and C) values that a thread loads
   static constexpr int YROW = CH + (LN > 1 ? 64 / LN : 0);  // LN token rows written at once: distinct banks
 };
 
+// v[i] of the LN lanes of a channel (lane bits 2 ..), summed over them: lane q of them returns the sum
+// of v[q].  Each step halves the values: a lane keeps those that its own bit selects.
+template <int LN>
+__device__ __forceinline__ float spread4(const float (&v)[LN], int q) {
+  if constexpr (LN == 1) {
+    return v[0];
+  } else {
+    constexpr int half = LN / 2;
+    float r[half];
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      if constexpr (LN >= 8) {  // the rows of 16 (halves of 32) trade places: one's own and the partner's values meet
+        const uint32_t a = __float_as_uint(v[i]), b = __float_as_uint(v[i + half]);
+        const auto w = LN == 16 ? __builtin_amdgcn_permlane32_swap(a, b, false, false) : __builtin_amdgcn_permlane16_swap(a, b, false, false);
+        r[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+      } else {
+        constexpr int kDown = LN == 4 ? 0x128 : 0x104, kUp = LN == 4 ? 0x128 : 0x114;  // lane ^ 8 by rotation; lane + 4, lane - 4
+        const float lo = v[i] + dpp<kDown>(v[i]), hi = v[i + half] + dpp<kUp>(v[i + half]);
+        r[i] = q & half ? hi : lo;
+      }
+    }
+    return spread4<half>(r, q);
+  }
+}
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// What four tokens need of LDS.
+template <int LN, bool CARRY>
+struct Quad {
+  float2 dx[4];
+  float b[4];
+  float4 c[4];
+  template <int CH, int NP>
+  __device__ __forceinline__ void load(const float2 (*s_dx)[CH], const float (*s_b)[NP], const float (*s_c)[NP], int t, int ch, int q, int j) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      dx[u] = s_dx[t + u][ch];
+      b[u] = s_b[t + u][4 * q + j];
+      if constexpr (!CARRY) c[u] = *reinterpret_cast<const float4 *>(&s_c[t + u][4 * q]);
+    }
+  }
+  // One token: the states' update and the lane's part of y.
+  __device__ __forceinline__ float step(int u, const float (&A)[4], f32x4 &h) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] *= __builtin_amdgcn_exp2f(dx[u].x * A[i]);
+    h = __builtin_amdgcn_mfma_f32_4x4x1f32(b[u], dx[u].y, h, 0, 0, 0);
+    if constexpr (CARRY) return 0.f;
+    else return fmaf(c[u].w, h[3], fmaf(c[u].z, h[2], fmaf(c[u].y, h[1], c[u].x * h[0])));
+  }
+};
+
 template <bool BF16, bool VEC, int LN, bool CARRY>
-__global__ void __launch_bounds__(256) ssm_scan_tile_kernel(ScanSsmParams p) {
+__global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(ScanSsmParams p) {
   using T = Tile<LN>;
-  constexpr int CH = T::CH, TT = T::TT, VW = T::VW, NI = T::NI, NP = T::NP, NBC = T::NBC;
-  __shared__ __align__(16) float2 s_dx[2][TT][CH];       // delta, delta x
-  __shared__ __align__(16) float s_bc[2][TT][2 * NP];    // B, C
+  constexpr int CH = T::CH, TT = T::TT, VW = T::VW, NI = T::NI, NP = T::NP, NB = T::NB;
+  __shared__ __align__(16) float2 s_dx[2][TT][CH];  // delta, delta x
+  __shared__ __align__(16) float s_b[2][TT][NP];
+  __shared__ __align__(16) float s_c[CARRY ? 1 : 2][CARRY ? 1 : TT][NP];
   __shared__ __align__(16) float s_y[CARRY ? 1 : 2][CARRY ? 1 : TT][T::YROW];
 
-  const int tid = threadIdx.x, q = tid % LN, ch = tid / LN;
+  const int tid = threadIdx.x & 255;
+  const bool scanning = uniform((int)(threadIdx.x >> 8)) == 0;
   const Sequence sq = find_sequence(p.seq, blockIdx.y, tid & 63);
   if (!sq.ok) return;
   const int seg = blockIdx.z, N = p.N;
@@ -151,163 +232,248 @@ __global__ void __launch_bounds__(256) ssm_scan_tile_kernel(ScanSsmParams p) {
   const int g = blockIdx.x / blocks, c_base = (blockIdx.x % blocks) * CH;
   const long d0 = (long)g * per_group + c_base;      // first channel of the workgroup
   const int c_live = min(CH, per_group - c_base);    // channels it has
-  const bool live = ch < c_live;
-  const long d = d0 + (live ? ch : 0);
-  const bool whole = (N & 3) == 0 && 4 * q < N;
+  const int tiles = (t_end - t_begin + TT - 1) / TT;
 
-  float A[4], h[4] = {0.f, 0.f, 0.f, 0.f}, total = 0.f;
-  load_state4(p.A + d * N, q, N, whole, A);
+  if (scanning) {
+    const int lane = tid & 63, j = lane & 3, q = (lane >> 2) % LN;
+    const int ch = (tid >> 6) * (64 / LN) + (lane >> 2) / LN * 4 + j;
+    const bool live = ch < c_live;
+    const long d = d0 + (live ? ch : 0);
+    const bool whole = (N & 3) == 0 && 4 * q < N;
+    float A[4], h0[4] = {0.f, 0.f, 0.f, 0.f}, total = 0.f;
+    load_state4(p.A + d * N, q, N, whole, A);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+    for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
 
-  const long slot = (long)p.D * N;  // workspace: [units][nseg][D][N] states, then [units][nseg - 1][D] sums
-  float *ws_h = p.workspace + (long)blockIdx.y * p.nseg * slot + d * N;
-  float *ws_s = p.workspace + (long)p.seq.units * p.nseg * slot + (long)blockIdx.y * (p.nseg - 1) * p.D + d;
-  if (CARRY || p.nseg == 1) {
-    if (seg == 0) {
-      if (p.seq.state_in) load_state4(p.seq.state_in + ((long)sq.row_in * p.D + d) * N, q, N, whole, h);
-      if (CARRY && live) store_state4(ws_h, q, N, whole, h);
-    }
-    if (CARRY && t_end == sq.len) return;  // its state is the main pass's own
-  } else {
-    load_state4(ws_h + (seg ? slot : 0), q, N, whole, h);
-    for (int k = 2; k <= seg; ++k) {
-      float part[4];
-      load_state4(ws_h + k * slot, q, N, whole, part);
-      const float sum = ws_s[(long)(k - 1) * p.D];
+    const long slot = (long)p.D * N;  // workspace: [units][nseg][D][N] states, then [units][nseg - 1][D] sums
+    float *ws_h = p.workspace + (long)blockIdx.y * p.nseg * slot + d * N;
+    float *ws_s = p.workspace + (long)p.seq.units * p.nseg * slot + (long)blockIdx.y * (p.nseg - 1) * p.D + d;
+    if (CARRY || p.nseg == 1) {
+      if (seg == 0) {
+        if (p.seq.state_in) load_state4(p.seq.state_in + ((long)sq.row_in * p.D + d) * N, q, N, whole, h0);
+        if (CARRY && live) store_state4(ws_h, q, N, whole, h0);
+      }
+    } else {
+      load_state4(ws_h + (seg ? slot : 0), q, N, whole, h0);
+      for (int k = 2; k <= seg; ++k) {
+        float part[4];
+        load_state4(ws_h + k * slot, q, N, whole, part);
+        const float sum = ws_s[(long)(k - 1) * p.D];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(sum * A[i]), h[i], part[i]);
+        for (int i = 0; i < 4; ++i) h0[i] = fmaf(__builtin_amdgcn_exp2f(sum * A[i]), h0[i], part[i]);
+      }
     }
+    if (CARRY && t_end == sq.len) return;  // its state is the main pass's own (the staging waves leave too)
+    // the states have arrived before the loop, which then waits for LDS only
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(h0[i]), "+v"(A[i]));
+    f32x4 h = {h0[0], h0[1], h0[2], h0[3]};
+    if (tiles > 0) __syncthreads();
+    for (int k = 0; k < tiles; ++k) {
+      const int buf = k & 1, cbuf = CARRY ? 0 : buf;
+      constexpr int S = LN > 8 ? LN : 8;  // LDS reads run four tokens ahead of the arithmetic
+      Quad<LN, CARRY> quad[2];
+      quad[0].load(s_dx[buf], s_b[buf], s_c[cbuf], 0, ch, q, j);
+#pragma unroll 1
+      for (int u0 = 0; u0 < TT; u0 += S) {
+        float part[LN > 4 ? LN : 4];
+#pragma unroll
+        for (int v = 0; v < S; v += 4) {
+          const int next = u0 + v + 4;
+          if (v + 4 < S || next < TT) quad[(v / 4 + 1) & 1].load(s_dx[buf], s_b[buf], s_c[cbuf], next, ch, q, j);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float y = quad[(v / 4) & 1].step(u, A, h);
+            if constexpr (CARRY) total += quad[(v / 4) & 1].dx[u].x;
+            else part[(LN > 4 ? v : 0) + u] = y;
+          }
+          if constexpr (!CARRY) {
+            if constexpr (LN <= 4) {
+#pragma unroll
+              for (int w = 0; w < 4; w += LN) {
+                float some[LN];
+#pragma unroll
+                for (int i = 0; i < LN; ++i) some[i] = part[w + i];
+                s_y[buf][u0 + v + w + q][ch] = spread4<LN>(some, q);
+              }
+            } else if (v + 4 == S) {
+              float some[LN];
+#pragma unroll
+              for (int i = 0; i < LN; ++i) some[i] = part[i];
+              s_y[buf][u0 + v + 4 - LN + q][ch] = spread4<LN>(some, q);
+            }
+          }
+        }
+      }
+      if constexpr (!CARRY) {
+        const int t = t_begin + (k + 1) * TT;
+        if (p.chunk_states && live && t % kScanChunk == 0 && t < sq.len) {
+          const float out[4] = {h[0], h[1], h[2], h[3]};
+          store_state4(p.chunk_states + (((long)blockIdx.y * p.n_chunks + t / kScanChunk - 1) * p.D + d) * N, q, N, whole, out);
+        }
+      }
+      __syncthreads();
+    }
+    const float out[4] = {h[0], h[1], h[2], h[3]};
+    if constexpr (CARRY) {
+      if (live) {
+        store_state4(ws_h + (seg + 1) * slot, q, N, whole, out);
+        if (q == 0) ws_s[(long)seg * p.D] = total;
+      }
+    } else if (live && t_end == sq.len && p.seq.state_out && !(sq.len == 0 && p.seq.state_out == p.seq.state_in)) {
+      store_state4(p.seq.state_out + ((long)sq.row_out * p.D + d) * N, q, N, whole, out);
+    }
+    return;
   }
 
-  // the loading layout: item i of a thread is VW adjacent channels of one token
-  constexpr int ROW = CH / VW;
+  // Staging waves.  Item i of a thread is VW adjacent channels of one token.
+  if (tiles == 0 || (CARRY && t_end == sq.len)) return;
+  constexpr int ROW = CH / VW, L_STEP = 256 / ROW, EL = BF16 ? 2 : 4;
   const int l_c = (tid % ROW) * VW, l_t = tid / ROW;
-  constexpr int L_STEP = 256 / ROW;
-  const int l_live = min(VW, c_live - l_c);
   float bias[VW], skip[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    bias[e] = p.dt_bias && e < l_live ? p.dt_bias[d0 + l_c + e] : 0.f;
-    skip[e] = p.skip && e < l_live ? p.skip[d0 + l_c + e] : 0.f;
+    const bool in = l_c + e < c_live;
+    bias[e] = p.dt_bias && in ? p.dt_bias[d0 + l_c + e] : 0.f;
+    skip[e] = p.skip && in ? p.skip[d0 + l_c + e] : 0.f;
   }
+  const auto columns = [&](int el, uint32_t (&col)[VEC ? 1 : VW]) {
+#pragma unroll
+    for (int e = 0; e < (VEC ? 1 : VW); ++e) col[e] = (l_c + e) * el + (l_c + e < c_live ? 0u : kOutside);
+  };
+  uint32_t col[VEC ? 1 : VW];
+  columns(EL, col);
   using Raw = RawRow<BF16, VEC, VW>;
-  Raw x[NI], dt[NI], z[NI], nx[NI], nz[NI];
-  float bc[NBC];
+  Raw x[NI], dt[NI], z[NI];                    // of the tile requested
+  Raw x_scan[NI], z_scan[NI], x_done[NI], z_done[NI];  // of the tile being scanned, and of the one before
+  uint32_t bb[NB] = {}, cc[NB] = {};
+  const bool gate = !CARRY && p.z.base;
+  const int b_n = tid % NP, b_t = tid / NP;  // B and C: state and token of this thread's first value
+  constexpr int B_STEP = 256 / NP;
+  const bool b_in = TT * NP >= 256 || b_t < TT;
+  const uint32_t b_col = b_n * EL + (b_n < N && b_in ? 0u : kOutside);
 
   const auto request = [&](int t0) {  // the loads of the tile at t0
+    const long row = sq.off + t0;
+    const int rows = min(TT, t_end - t0);
+    const auto wx = window<EL>(p.x.base, p.x.stride, row, rows, d0, c_live);
+    const auto wd = window<EL>(p.dt.base, p.dt.stride, row, rows, d0, c_live);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int t = t0 + l_t + i * L_STEP;
-      const int n = t < t_end ? l_live : 0;
-      nx[i].load(p.x, sq.off + t, d0 + l_c, n);
-      dt[i].load(p.dt, sq.off + t, d0 + l_c, n);
-      if (!CARRY && p.z.base) nz[i].load(p.z, sq.off + t, d0 + l_c, n);
+      const uint32_t t = l_t + i * L_STEP;
+      x[i].load(wx, t * (uint32_t)p.x.stride * EL, col);
+      dt[i].load(wd, t * (uint32_t)p.dt.stride * EL, col);
     }
+    if (gate) {
+      const auto wz = window<EL>(p.z.base, p.z.stride, row, rows, d0, c_live);
 #pragma unroll
-    for (int i = 0; i < NBC; ++i) {
-      const int e = tid + i * 256, n = e % NP, which = (e / NP) & 1, t = t0 + e / (2 * NP);
-      bc[i] = 0.f;
-      if (e < TT * 2 * NP && n < N && t < t_end && !(CARRY && which)) {
-        const TokenArray &a = which ? p.Cm : p.Bm;
-        bc[i] = load1<BF16>(a.base, (sq.off + t) * a.stride + (long)g * N + n);
+      for (int i = 0; i < NI; ++i) z[i].load(wz, (l_t + i * L_STEP) * (uint32_t)p.z.stride * EL, col);
+    }
+    const auto wb = window<EL>(p.Bm.base, p.Bm.stride, row, rows, (long)g * N, N);
+    const auto wc = window<EL>(p.Cm.base, p.Cm.stride, row, rows, (long)g * N, N);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const uint32_t t = b_t + i * B_STEP;
+      const int ob = (int)(t * (uint32_t)p.Bm.stride * EL + b_col), oc = (int)(t * (uint32_t)p.Cm.stride * EL + b_col);
+      if constexpr (BF16) {
+        bb[i] = __builtin_amdgcn_raw_buffer_load_b16(wb, ob, 0, 0);
+        if constexpr (!CARRY) cc[i] = __builtin_amdgcn_raw_buffer_load_b16(wc, oc, 0, 0);
+      } else {
+        bb[i] = __builtin_amdgcn_raw_buffer_load_b32(wb, ob, 0, 0);
+        if constexpr (!CARRY) cc[i] = __builtin_amdgcn_raw_buffer_load_b32(wc, oc, 0, 0);
       }
     }
   };
   const auto stage = [&](int t0, int buf) {  // delta, delta x, B and C of the requested tile
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const bool in = t0 + l_t + i * L_STEP < t_end;
+      dt[i].arrive(); x[i].arrive();
+      if (gate) z[i].arrive();
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(bb[i]), "+v"(cc[i]));
+    float delta[NI][VW];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) delta[i][e] = dt[i].get(e) + bias[e];
+    if (p.softplus) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) delta[i][e] = softplus_f(delta[i][e]);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bool in = t0 + l_t + i * L_STEP < t_end;  // a token past the end leaves the state as it is
       float2 *row = &s_dx[buf][l_t + i * L_STEP][l_c];
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        const float raw = dt[i].get(e) + bias[e];
-        // a token past the end leaves the state as it is
-        const float delta = in ? (p.softplus ? softplus_f(raw) : raw) : 0.f;
-        row[e] = make_float2(delta, delta * nx[i].get(e));
+        const float v = in ? delta[i][e] : 0.f;
+        row[e] = make_float2(v, v * x[i].get(e));
       }
     }
 #pragma unroll
-    for (int i = 0; i < NBC; ++i) {
-      const int e = tid + i * 256;
-      if (e < TT * 2 * NP) s_bc[buf][e / (2 * NP)][e % (2 * NP)] = bc[i];
+    for (int i = 0; i < NB; ++i) {
+      const int t = (b_t + i * B_STEP) & (TT - 1);
+      if (b_in) {
+        s_b[buf][t][b_n] = BF16 ? bf16_lo(bb[i]) : __uint_as_float(bb[i]);
+        if constexpr (!CARRY) s_c[buf][t][b_n] = BF16 ? bf16_lo(cc[i]) : __uint_as_float(cc[i]);
+      }
+    }
+  };
+  const auto finish = [&](int t0, int buf) {  // the results of the tile at t0, from the sums of its scan
+    float y[NI][VW];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) y[i][e] = fmaf(skip[e], x_done[i].get(e), s_y[buf][l_t + i * L_STEP][l_c + e]);
+    if (gate) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) y[i][e] *= z_done[i].get(e) * sigmoid_f(z_done[i].get(e));
+    }
+    const long row = sq.off + t0;
+    const int rows = min(TT, t_end - t0);
+    uint32_t to[VEC ? 1 : VW];
+    if (p.y_bf16) {
+      columns(2, to);
+      const auto wy = window<2>(p.y, p.D, row, rows, d0, c_live);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) store_row<true, VEC, VW>(wy, (l_t + i * L_STEP) * (uint32_t)p.D * 2, to, y[i]);
+    } else {
+      columns(4, to);
+      const auto wy = window<4>(p.y, p.D, row, rows, d0, c_live);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) store_row<false, VEC, VW>(wy, (l_t + i * L_STEP) * (uint32_t)p.D * 4, to, y[i]);
     }
   };
 
   request(t_begin);
   stage(t_begin, 0);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) { x[i] = nx[i]; z[i] = nz[i]; }
+  for (int i = 0; i < NI; ++i) { x_scan[i] = x_done[i] = x[i]; z_scan[i] = z_done[i] = z[i]; }
+  if (tiles > 1) request(t_begin + TT);
   __syncthreads();
-  int buf = 0;
-  for (int t0 = t_begin; t0 < t_end; t0 += TT, buf ^= 1) {
-    const bool more = t0 + TT < t_end;
-    if (more) request(t0 + TT);
-#pragma unroll 1
-    for (int u0 = 0; u0 < TT; u0 += LN) {
-      float part[LN];
-#pragma unroll
-      for (int u = 0; u < LN; ++u) {
-        const float2 dx = s_dx[buf][u0 + u][ch];
-        const float4 B = *reinterpret_cast<const float4 *>(&s_bc[buf][u0 + u][4 * q]);
-        const float b[4] = {B.x, B.y, B.z, B.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(dx.x * A[i]), h[i], dx.y * b[i]);
-        if constexpr (CARRY) {
-          total += dx.x;
-        } else {
-          const float4 C = *reinterpret_cast<const float4 *>(&s_bc[buf][u0 + u][NP + 4 * q]);
-          part[u] = fmaf(C.w, h[3], fmaf(C.z, h[2], fmaf(C.y, h[1], C.x * h[0])));
-        }
-      }
-      if constexpr (!CARRY) s_y[buf][u0 + q][ch] = sum_spread<LN>(part, q);
-    }
+  for (int k = 0; k < tiles; ++k) {
+    const int t0 = t_begin + k * TT;
+    if (!CARRY && k) finish(t0 - TT, (k - 1) & 1);
     if constexpr (!CARRY) {
-      if (p.chunk_states && live && (t0 + TT) % kScanChunk == 0 && t0 + TT < sq.len)
-        store_state4(p.chunk_states + (((long)blockIdx.y * p.n_chunks + (t0 + TT) / kScanChunk - 1) * p.D + d) * N, q, N, whole, h);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) { x_done[i] = x_scan[i]; z_done[i] = z_scan[i]; }
     }
-    if (more) stage(t0 + TT, buf ^ 1);
+    if (k + 1 < tiles) {
+      stage(t0 + TT, (k + 1) & 1);
+      if constexpr (!CARRY) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) { x_scan[i] = x[i]; z_scan[i] = z[i]; }
+      }
+      if (k + 2 < tiles) request(t0 + 2 * TT);
+    }
     __syncthreads();
-    if constexpr (!CARRY) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int t = l_t + i * L_STEP;
-        float y[VW];
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          y[e] = fmaf(skip[e], x[i].get(e), s_y[buf][t][l_c + e]);
-          if (p.z.base) {
-            const float zv = z[i].get(e);
-            y[e] *= zv * sigmoid_f(zv);
-          }
-        }
-        if (t0 + t < t_end) {
-          const long at = (sq.off + t0 + t) * p.D + d0 + l_c;
-          if constexpr (VEC) {
-            if (l_live > 0) {
-              if (p.y_bf16) storev<true, VW>(p.y, at, y);
-              else storev<false, VW>(p.y, at, y);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < VW; ++e)
-              if (e < l_live) store1(p.y, at + e, p.y_bf16, y[e]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NI; ++i) { x[i] = nx[i]; z[i] = nz[i]; }
   }
-
-  if constexpr (CARRY) {
-    if (live) {
-      store_state4(ws_h + (seg + 1) * slot, q, N, whole, h);
-      if (q == 0) ws_s[(long)seg * p.D] = total;
-    }
-  } else if (live && t_end == sq.len && p.seq.state_out && !(sq.len == 0 && p.seq.state_out == p.seq.state_in)) {
-    store_state4(p.seq.state_out + ((long)sq.row_out * p.D + d) * N, q, N, whole, h);
-  }
+  if constexpr (!CARRY) finish(t_begin + (tiles - 1) * TT, (tiles - 1) & 1);
 }
 
 template <bool BF16, int LN>
@@ -324,14 +490,14 @@ hipError_t go(const ScanSsmParams &p, hipStream_t s) {
   const bool vec = per_group % VW == 0 && fits(p.x) && fits(p.dt) && fits(p.z);
   if (p.nseg > 1) {
     const dim3 grid(blocks, p.seq.units, p.nseg - 1);
-    if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, true>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, true>), grid, dim3(256), 0, s, p);
+    if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, true>), grid, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, true>), grid, dim3(512), 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const dim3 grid(blocks, p.seq.units, p.nseg);
-  if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, false>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, false>), grid, dim3(256), 0, s, p);
+  if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, false>), grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, false>), grid, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
