@@ -69,10 +69,37 @@ WKV_API wkv_status wkv_ssm_conv_forward_varlen(int num_slots, int D, int W,
                         const float *state_in, float *state_out, const int32_t *state_map,
                         int n_state, int32_t *dev_status, void *stream);
 
+/* Bytes of workspace of wkv_ssm_conv_backward.  Pure host function. */
+WKV_API size_t wkv_ssm_conv_backward_workspace(int B, int T, int D, int W);
+
+/*
+ * Gradients of wkv_ssm_conv_forward (the same inputs; T >= 1) for the loss
+ * L = sum(dy * y) + sum(d_state_out * final state):
+ *   dy         [B,T,D] dy_dtype, row stride dy_stride
+ *   d_state_out [B,W-1,D] fp32 or NULL (zero)
+ *   dx         [B,T,D] grad_dtype
+ *   d_weight [D,W], d_bias [D] (NULL: not wanted) fp32, summed over the batch
+ *   d_state_in [B,W-1,D] fp32 or NULL: gradient of the initial state row b
+ *              started from (rows that share one are not summed)
+ *   workspace  16-byte aligned, at least wkv_ssm_conv_backward_workspace(...)
+ *              bytes, as in wkv_ssm_scan_backward
+ * A row whose state_map entry is outside the table sets WKV_DEV_BAD_STATE_MAP
+ * and has no share in the summed gradients; its own rows are not written.
+ */
+WKV_API wkv_status wkv_ssm_conv_backward(int B, int T, int D, int W,
+                        const void *x, int64_t x_stride, wkv_dtype in_dtype,
+                        const float *weight, const float *bias, wkv_activation act,
+                        const void *dy, int64_t dy_stride, wkv_dtype dy_dtype,
+                        const float *state_in, const int32_t *state_map, int n_state,
+                        const float *d_state_out, void *dx, wkv_dtype grad_dtype,
+                        float *d_weight, float *d_bias, float *d_state_in,
+                        void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
 /* Bytes of workspace with which a scan of `rows` sequences (batch rows or
- * slots) of up to T tokens is cut into segments that run side by side: 0 where
- * the rows alone fill the chip, and for T <= 64.  Pure host function. */
-WKV_API size_t wkv_ssm_scan_workspace(int rows, int T, int D, int N, int G);
+ * slots) of up to T tokens, total_tokens in all, is cut into segments that run
+ * side by side: 0 where the rows alone fill the chip, and for T <= 64.  Pure
+ * host function. */
+WKV_API size_t wkv_ssm_scan_workspace(int rows, int T, int64_t total_tokens, int D, int N, int G);
 
 /*
  * Selective scan.  D channels in G equal groups that share B and C; state
@@ -89,7 +116,7 @@ WKV_API size_t wkv_ssm_scan_workspace(int rows, int T, int D, int N, int G);
  *   state_in   [n_state,D,N] fp32 or NULL (zeros); state_map, n_state, state_out
  *              ([B,D,N]), dev_status as wkv_ssm_conv_forward
  *   workspace  16-byte aligned device memory of at least
- *              wkv_ssm_scan_workspace(B, T, D, N, G) bytes, whose content does not
+ *              wkv_ssm_scan_workspace(B, T, B*T, D, N, G) bytes, whose content does not
  *              matter and which no other call may use until this one is done; NULL:
  *              the sequences are not cut (slower where they are few and long)
  * A token whose delta is 0 (dt = -inf under the softplus) leaves the state as
@@ -105,8 +132,59 @@ WKV_API wkv_status wkv_ssm_scan_forward(int B, int T, int D, int N, int G,
                         float *state_out, void *workspace, size_t workspace_bytes,
                         int32_t *dev_status, void *stream);
 
-/* The same for slots: token arrays are packed [total_tokens, ..]; slot s reads
- * and writes state row state_map[s] (NULL: s) of [n_state,D,N]. */
+/* wkv_ssm_scan_forward that also saves the state at every 16-token boundary for
+ * wkv_ssm_scan_backward (y and state_out are bitwise those of that call):
+ *   chunk_states [B,ceil(T/16)-1,D,N] fp32, 16-byte aligned (may be NULL when
+ *              T <= 16): entry c-1 is the state after token 16c-1 */
+WKV_API wkv_status wkv_ssm_scan_forward_train(int B, int T, int D, int N, int G,
+                        const void *x, int64_t x_stride, const void *dt, int64_t dt_stride,
+                        const float *A, const void *Bm, int64_t b_stride,
+                        const void *Cm, int64_t c_stride, wkv_dtype in_dtype,
+                        const float *skip, const void *z, int64_t z_stride,
+                        const float *dt_bias, int dt_softplus, void *y, wkv_dtype out_dtype,
+                        const float *state_in, const int32_t *state_map, int n_state,
+                        float *state_out, float *chunk_states, void *workspace, size_t workspace_bytes,
+                        int32_t *dev_status, void *stream);
+
+/* Bytes of workspace of wkv_ssm_scan_backward, with the forward call's chunk
+ * states at hand or without.  Pure host function. */
+WKV_API size_t wkv_ssm_scan_backward_workspace(int B, int T, int D, int N, int G, int with_chunk_states);
+
+/*
+ * Gradients of wkv_ssm_scan_forward (the same inputs; T >= 1) for the loss
+ * L = sum(dy * y) + sum(d_state_out * final state):
+ *   dy         [B,T,D] dy_dtype, row stride dy_stride
+ *   chunk_states  what wkv_ssm_scan_forward_train saved for these inputs, or
+ *              NULL: they are computed first
+ *   d_state_out [B,D,N] fp32 or NULL (zero)
+ *   dx, ddt, dz  [B,T,D] grad_dtype, 16-byte aligned (dz: NULL exactly when z is)
+ *   dB, dC     [B,T,G*N] grad_dtype, summed over the channels of a group
+ *   dA [D,N], d_skip [D] (NULL: not wanted), d_dt_bias [D] (NULL: not wanted)
+ *              fp32, summed over the batch
+ *   d_state_in [B,D,N] fp32 or NULL: gradient of the initial state row b
+ *              started from (rows that share one are not summed)
+ *   workspace  16-byte aligned, at least wkv_ssm_scan_backward_workspace(...)
+ *              bytes; its content does not matter, and no other call may use it
+ *              until this one is done
+ * Sums run in fp32 and in one order.  A row whose state_map entry is outside
+ * the table sets WKV_DEV_BAD_STATE_MAP and has no share in the summed
+ * gradients; its own rows are not written.
+ */
+WKV_API wkv_status wkv_ssm_scan_backward(int B, int T, int D, int N, int G,
+                        const void *x, int64_t x_stride, const void *dt, int64_t dt_stride,
+                        const float *A, const void *Bm, int64_t b_stride,
+                        const void *Cm, int64_t c_stride, wkv_dtype in_dtype,
+                        const float *skip, const void *z, int64_t z_stride,
+                        const float *dt_bias, int dt_softplus,
+                        const void *dy, int64_t dy_stride, wkv_dtype dy_dtype,
+                        const float *state_in, const int32_t *state_map, int n_state,
+                        const float *chunk_states, const float *d_state_out,
+                        void *dx, void *ddt, void *dB, void *dC, void *dz, wkv_dtype grad_dtype,
+                        float *dA, float *d_skip, float *d_dt_bias, float *d_state_in,
+                        void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* wkv_ssm_scan_forward for slots: token arrays are packed [total_tokens, ..];
+ * slot s reads and writes state row state_map[s] (NULL: s) of [n_state,D,N]. */
 WKV_API wkv_status wkv_ssm_scan_forward_varlen(int num_slots, int D, int N, int G,
                         const int32_t *lengths, int max_len, int total_tokens,
                         const void *x, int64_t x_stride, const void *dt, int64_t dt_stride,

@@ -57,6 +57,7 @@ SIGNATURES = {
 
 # mirrors include/wkv_ssm.h
 _l = ctypes.c_int64
+_sz = ctypes.c_size_t
 _seq_dense = [_vp, _vp, _i, _vp, _vp, _vp]       # state_in, state_map, n_state, state_out, dev_status, stream
 _seq_slots = [_vp, _vp, _vp, _i, _vp, _vp]       # state_in, state_out, state_map, n_state, dev_status, stream
 _conv = [_vp, _l, _i, _vp, _vp, _i, _vp, _i]     # x, stride, dtype, weight, bias, act, y, out dtype
@@ -65,9 +66,16 @@ _store = [_vp, _vp, _i, _i, _vp, _i, _l, _vp, _vp, _i, _vp, _vp]
 SSM_SIGNATURES = {
     "wkv_ssm_conv_forward": (_i, [_i] * 4 + _conv + _seq_dense),
     "wkv_ssm_conv_forward_varlen": (_i, [_i] * 3 + [_vp, _i, _i] + _conv + _seq_slots),
-    "wkv_ssm_scan_workspace": (ctypes.c_size_t, [_i] * 5),
-    "wkv_ssm_scan_forward": (_i, [_i] * 5 + _scan + [_vp, _i] + _seq_dense[:4] + [_vp, ctypes.c_size_t, _vp, _vp]),
-    "wkv_ssm_scan_forward_varlen": (_i, [_i] * 4 + [_vp, _i, _i] + _scan + [_vp, _i] + _seq_slots[:4] + [_vp, ctypes.c_size_t, _vp, _vp]),
+    "wkv_ssm_conv_backward_workspace": (_sz, [_i] * 4),
+    "wkv_ssm_conv_backward": (_i, [_i] * 4 + _conv[:6] + [_vp, _l, _i] + _seq_dense[:3] + [_vp, _vp, _i, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "wkv_ssm_scan_workspace": (_sz, [_i, _i, _l, _i, _i, _i]),
+    "wkv_ssm_scan_forward_train": (_i, [_i] * 5 + _scan + [_vp, _i] + _seq_dense[:4] + [_vp, _vp, _sz, _vp, _vp]),
+    "wkv_ssm_scan_backward_workspace": (_sz, [_i] * 6),
+    # .. dy, states in, chunk states, d_state_out, token gradients, parameter gradients, workspace
+    "wkv_ssm_scan_backward": (_i, [_i] * 5 + _scan + [_vp, _l, _i] + _seq_dense[:3] + [_vp, _vp] + [_vp] * 5 + [_i] + [_vp] * 4
+                              + [_vp, _sz, _vp, _vp]),
+    "wkv_ssm_scan_forward": (_i, [_i] * 5 + _scan + [_vp, _i] + _seq_dense[:4] + [_vp, _sz, _vp, _vp]),
+    "wkv_ssm_scan_forward_varlen": (_i, [_i] * 4 + [_vp, _i, _i] + _scan + [_vp, _i] + _seq_slots[:4] + [_vp, _sz, _vp, _vp]),
     "wkv_state_store_write": (_i, _store),
     "wkv_state_store_read": (_i, _store),
 }

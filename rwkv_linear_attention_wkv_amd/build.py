@@ -23,7 +23,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libwkv.so")
 SOURCES = ["wkv_api.cpp", "wkv4_scan.hip", "wkv56_scan.hip", "wkv6_decode.hip", "wkv6_backward.hip", "wkv6_backward_chunked.hip", "wkv56_chunked.hip", "wkv6_chunked_save.hip",
            "wkv7_scan.hip", "wkv7_chunked.hip",
-           "ssm_api.cpp", "ssm_conv.hip", "ssm_scan.hip", "state_store.hip"]
+           "ssm_api.cpp", "ssm_conv.hip", "ssm_scan.hip", "ssm_scan_backward.hip", "state_store.hip"]
 ARCH = "gfx950"
 
 

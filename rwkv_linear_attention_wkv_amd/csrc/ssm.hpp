@@ -62,22 +62,45 @@ struct ScanSsmParams {
   bool softplus;
   void *y;
   bool y_bf16;
-  // null, or [units, n_chunks, D, N]: the state at the start of each 32-token chunk but the first
+  // null, or [units, n_chunks, D, N]: the state at the start of each 16-token chunk but the first;
+  // with y null these are all that is computed
   float *chunk_states;
   int n_chunks;
   int seg_len, nseg;  // tokens of a segment; with nseg > 1 the workspace holds the segments' states
   float *workspace;   // [units][nseg][D][N] states, [units][nseg - 1][D] sums of delta
 };
 
-constexpr int kScanChunk = 32;  // tokens between saved states
+constexpr int kScanChunk = 16;  // tokens between saved states
 constexpr int kScanShort = 8;   // calls of at most this many tokens a sequence take the kernel without tiles
 constexpr int kScanSplit = 64;  // a segment is a multiple of this; no shorter sequence is split
 
 // Lanes that share a channel, four states each.
 inline int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
-int scan_segments(int units, int T, int D, int N, int G, int *seg_len);
+int scan_segments(int units, int T, long total, int D, int N, int G, int *seg_len);
 hipError_t launch_ssm_scan(const ScanSsmParams &p, bool bf16, hipStream_t s);
+
+// The scan's backward pass, dense rows.
+struct ScanBackwardParams {
+  ScanSsmParams f;  // the forward call: its sequences (state_out unused), arrays and chunk states
+  TokenArray dy;
+  bool dy_bf16;
+  const float *d_state_out;  // [B, D, N] gradient of the final state, or null
+  void *dx, *ddt, *dz, *dB, *dC;  // contiguous, bf16 when grad_bf16
+  bool grad_bf16;
+  float *dA, *d_skip, *d_bias, *d_state_in;
+  int seg_len, nseg;
+  // workspace
+  float *carry;     // [B][nseg][D][N] states' gradients at the start of a segment from one of zero at
+                    // its end, then [B][nseg][D] sums of delta
+  float *part_A;    // [B * nseg][D][N]
+  float *part_ch;   // [B * nseg][2][D]: d_skip, d_bias
+  float *part_bc;   // [blocks of a group][B * T][G][2 N]: dB, dC of one block of channels
+};
+
+int backward_segments(int units, int T, int D, int N, int G, int *seg_len);
+int backward_blocks(int D, int N, int G);  // blocks of channels of a group
+hipError_t launch_ssm_scan_backward(const ScanBackwardParams &p, bool bf16, hipStream_t s);
 
 // The 8-bit state store: rows of `row` values in groups of 64 with one scale each.
 struct StoreParams {

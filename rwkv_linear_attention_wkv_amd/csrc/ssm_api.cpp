@@ -76,16 +76,22 @@ wkv_status token_array(const char *fn, const char *name, const void *base, int64
     if (st_ != WKV_OK) return st_;    \
   } while (0)
 
-wkv_status conv(const char *fn, const wkv::SeqParams &seq, int D, int W, const void *x, int64_t x_stride,
-                wkv_dtype in_dtype, const float *weight, const float *bias, wkv_activation act, void *y,
-                wkv_dtype out_dtype, void *stream) {
+wkv_status conv_checks(const char *fn, int D, int W, wkv_dtype in_dtype, const float *weight, const float *bias,
+                       wkv_activation act) {
   REQUIRE(D >= 1 && D <= kMaxChannels, "%s: need 1 <= D <= %d (got %d)", fn, kMaxChannels, D);
   if (W < 2 || W > 4) return fail(WKV_ERR_UNSUPPORTED, "%s: W=%d is not supported (2, 3 or 4)", fn, W);
   if (!dtype_ok(in_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown input dtype %d", fn, in_dtype);
-  if (!dtype_ok(out_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, out_dtype);
   if (act != WKV_ACT_NONE && act != WKV_ACT_SILU) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, act);
-  if (seq.units == 0) return ok();
   REQUIRE(weight && aligned(weight, 4) && aligned(bias, 4), "%s: weight must be given; weight and bias 4-byte aligned", fn);
+  return WKV_OK;
+}
+
+wkv_status conv(const char *fn, const wkv::SeqParams &seq, int D, int W, const void *x, int64_t x_stride,
+                wkv_dtype in_dtype, const float *weight, const float *bias, wkv_activation act, void *y,
+                wkv_dtype out_dtype, void *stream) {
+  CHECK(conv_checks(fn, D, W, in_dtype, weight, bias, act));
+  if (!dtype_ok(out_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, out_dtype);
+  if (seq.units == 0) return ok();
   if (seq.total_tokens > 0) {
     CHECK(token_array(fn, "x", x, x_stride, D, in_dtype));
     REQUIRE(y && aligned(y, 16), "%s: y must be non-NULL and 16-byte aligned", fn);
@@ -106,6 +112,39 @@ wkv_status conv(const char *fn, const wkv::SeqParams &seq, int D, int W, const v
 
 size_t scan_workspace(int units, int nseg, int D, int N) {
   return nseg > 1 ? sizeof(float) * (size_t)units * ((size_t)nseg * D * N + (size_t)(nseg - 1) * D) : 0;
+}
+
+int chunks_of(int T) { return T > 0 ? (T + wkv::kScanChunk - 1) / wkv::kScanChunk - 1 : 0; }
+
+// The backward pass's workspace, in floats from its start; each part starts at a multiple of four.
+struct BackwardSpace {
+  size_t carry, part_A, part_ch, part_bc, chunks, total;
+  int nseg, seg_len;
+};
+
+BackwardSpace backward_space(int B, int T, int D, int N, int G, bool with_chunks) {
+  BackwardSpace w{};
+  size_t at = 0;
+  const auto take = [&at](size_t floats) {
+    const size_t here = at;
+    at += (floats + 3) / 4 * 4;
+    return here;
+  };
+  w.nseg = wkv::backward_segments(B, T, D, N, G, &w.seg_len);
+  const size_t row = (size_t)D * N, parts = (size_t)B * w.nseg;
+  size_t carry = w.nseg > 1 ? parts * (row + D) : 0;
+  if (!with_chunks) {  // the forward pass's segments use the same part before it
+    int len;
+    const size_t fwd = scan_workspace(B, wkv::scan_segments(B, T, (long)B * T, D, N, G, &len), D, N) / sizeof(float);
+    if (fwd > carry) carry = fwd;
+  }
+  w.carry = take(carry);
+  w.part_A = take(parts * row);
+  w.part_ch = take(parts * 2 * D);
+  w.part_bc = take((size_t)wkv::backward_blocks(D, N, G) * B * T * G * 2 * N);
+  w.chunks = take(with_chunks ? 0 : (size_t)B * chunks_of(T) * row);
+  w.total = at;
+  return w;
 }
 
 // Checks shared by the scan's calls, and their parameters.
@@ -149,7 +188,7 @@ wkv_status scan(const char *fn, wkv::ScanSsmParams &p, wkv_dtype in_dtype, void 
     return ok();
   }
   p.y = y; p.y_bf16 = out_dtype == WKV_BF16;
-  p.nseg = wkv::scan_segments(p.seq.units, p.seq.T, p.D, p.N, p.G, &p.seg_len);
+  p.nseg = wkv::scan_segments(p.seq.units, p.seq.T, p.seq.total_tokens, p.D, p.N, p.G, &p.seg_len);
   if (p.nseg > 1) {
     const size_t need = scan_workspace(p.seq.units, p.nseg, p.D, p.N);
     if (workspace) {
@@ -210,10 +249,51 @@ wkv_status wkv_ssm_conv_forward_varlen(int num_slots, int D, int W, const int32_
   return conv(fn, seq, D, W, x, x_stride, in_dtype, weight, bias, act, y, out_dtype, stream);
 }
 
-size_t wkv_ssm_scan_workspace(int rows, int T, int D, int N, int G) {
-  if (rows < 1 || T < 1 || D < 1 || N < 1 || N > kMaxStates || G < 1 || D % G) return 0;
+size_t wkv_ssm_conv_backward_workspace(int B, int T, int D, int W) {
+  if (B < 1 || T < 1 || D < 1 || W < 2 || W > 4) return 0;
   int len;
-  return scan_workspace(rows, wkv::scan_segments(rows, T, D, N, G, &len), D, N);
+  return sizeof(float) * (size_t)B * wkv::conv_segments(B, T, D, true, &len) * (W + 1) * D;
+}
+
+wkv_status wkv_ssm_conv_backward(int B, int T, int D, int W, const void *x, int64_t x_stride, wkv_dtype in_dtype,
+                                 const float *weight, const float *bias, wkv_activation act, const void *dy,
+                                 int64_t dy_stride, wkv_dtype dy_dtype, const float *state_in,
+                                 const int32_t *state_map, int n_state, const float *d_state_out, void *dx,
+                                 wkv_dtype grad_dtype, float *d_weight, float *d_bias, float *d_state_in,
+                                 void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  const char *fn = "wkv_ssm_conv_backward";
+  REQUIRE(T >= 1, "%s: need T >= 1 (got %d)", fn, T);
+  wkv::ConvParams p{};
+  CHECK(dense_seq(fn, B, T, state_in, state_map, n_state, nullptr, dev_status, &p.seq));
+  CHECK(conv_checks(fn, D, W, in_dtype, weight, bias, act));
+  if (!dtype_ok(dy_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown dtype of dy %d", fn, dy_dtype);
+  if (!dtype_ok(grad_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown gradient dtype %d", fn, grad_dtype);
+  CHECK(token_array(fn, "x", x, x_stride, D, in_dtype));
+  CHECK(token_array(fn, "dy", dy, dy_stride, D, dy_dtype));
+  REQUIRE(dx && d_weight, "%s: dx and d_weight must be non-NULL", fn);
+  REQUIRE(aligned(dx, 16) && aligned(d_weight, 4) && aligned(d_bias, 4) && aligned(d_state_in, 16) && aligned(d_state_out, 16),
+          "%s: dx and the states' gradients must be 16-byte aligned, d_weight and d_bias 4-byte aligned", fn);
+  REQUIRE(dx != x && dx != dy, "%s: dx may not overlap an input", fn);
+  const size_t need = wkv_ssm_conv_backward_workspace(B, T, D, W);
+  REQUIRE(workspace && aligned(workspace, 16) && workspace_bytes >= need,
+          "%s: the workspace must be 16-byte aligned and hold %zu bytes (got %zu)", fn, need, workspace_bytes);
+  p.D = D; p.W = W;
+  p.x = {x, (long)x_stride};
+  p.weight = weight; p.bias = bias;
+  p.silu = act == WKV_ACT_SILU;
+  p.y = dx; p.y_bf16 = grad_dtype == WKV_BF16;
+  p.dy = {dy, (long)dy_stride}; p.dy_bf16 = dy_dtype == WKV_BF16;
+  p.d_state_out = d_state_out; p.d_state_in = d_state_in;
+  p.partial = static_cast<float *>(workspace);
+  p.d_weight = d_weight; p.d_bias = d_bias;
+  p.nseg = wkv::conv_segments(B, T, D, true, &p.seg_len);
+  return launched(wkv::launch_ssm_conv_backward(p, in_dtype == WKV_BF16, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t wkv_ssm_scan_workspace(int rows, int T, int64_t total_tokens, int D, int N, int G) {
+  if (rows < 1 || T < 1 || total_tokens < 0 || D < 1 || N < 1 || N > kMaxStates || G < 1 || D % G) return 0;
+  int len;
+  return scan_workspace(rows, wkv::scan_segments(rows, T, (long)total_tokens, D, N, G, &len), D, N);
 }
 
 wkv_status wkv_ssm_scan_forward(int B, int T, int D, int N, int G, const void *x, int64_t x_stride, const void *dt,
@@ -230,6 +310,90 @@ wkv_status wkv_ssm_scan_forward(int B, int T, int D, int N, int G, const void *x
   CHECK(scan_params(fn, seq, D, N, G, x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, in_dtype, skip, z,
                     z_stride, dt_bias, dt_softplus, &p));
   return scan(fn, p, in_dtype, y, out_dtype, workspace, workspace_bytes, stream);
+}
+
+wkv_status wkv_ssm_scan_forward_train(int B, int T, int D, int N, int G, const void *x, int64_t x_stride,
+                                      const void *dt, int64_t dt_stride, const float *A, const void *Bm,
+                                      int64_t b_stride, const void *Cm, int64_t c_stride, wkv_dtype in_dtype,
+                                      const float *skip, const void *z, int64_t z_stride, const float *dt_bias,
+                                      int dt_softplus, void *y, wkv_dtype out_dtype, const float *state_in,
+                                      const int32_t *state_map, int n_state, float *state_out, float *chunk_states,
+                                      void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  const char *fn = "wkv_ssm_scan_forward_train";
+  wkv::SeqParams seq;
+  CHECK(dense_seq(fn, B, T, state_in, state_map, n_state, state_out, dev_status, &seq));
+  wkv::ScanSsmParams p;
+  CHECK(scan_params(fn, seq, D, N, G, x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, in_dtype, skip, z,
+                    z_stride, dt_bias, dt_softplus, &p));
+  p.n_chunks = chunks_of(T);
+  if (p.n_chunks > 0) {
+    REQUIRE(chunk_states && aligned(chunk_states, 16),
+            "%s: chunk_states must be a non-NULL, 16-byte aligned device array (T > %d)", fn, wkv::kScanChunk);
+    p.chunk_states = chunk_states;
+  }
+  return scan(fn, p, in_dtype, y, out_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t wkv_ssm_scan_backward_workspace(int B, int T, int D, int N, int G, int with_chunk_states) {
+  if (B < 1 || T < 1 || D < 1 || N < 1 || N > kMaxStates || G < 1 || D % G) return 0;
+  return sizeof(float) * backward_space(B, T, D, N, G, with_chunk_states != 0).total;
+}
+
+wkv_status wkv_ssm_scan_backward(int B, int T, int D, int N, int G, const void *x, int64_t x_stride, const void *dt,
+                                 int64_t dt_stride, const float *A, const void *Bm, int64_t b_stride,
+                                 const void *Cm, int64_t c_stride, wkv_dtype in_dtype, const float *skip,
+                                 const void *z, int64_t z_stride, const float *dt_bias, int dt_softplus,
+                                 const void *dy, int64_t dy_stride, wkv_dtype dy_dtype, const float *state_in,
+                                 const int32_t *state_map, int n_state, const float *chunk_states,
+                                 const float *d_state_out, void *dx, void *ddt, void *dB, void *dC, void *dz,
+                                 wkv_dtype grad_dtype, float *dA, float *d_skip, float *d_dt_bias,
+                                 float *d_state_in, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                 void *stream) {
+  const char *fn = "wkv_ssm_scan_backward";
+  REQUIRE(T >= 1, "%s: need T >= 1 (got %d)", fn, T);
+  wkv::SeqParams seq;
+  CHECK(dense_seq(fn, B, T, state_in, state_map, n_state, nullptr, dev_status, &seq));
+  wkv::ScanBackwardParams p{};
+  CHECK(scan_params(fn, seq, D, N, G, x, x_stride, dt, dt_stride, A, Bm, b_stride, Cm, c_stride, in_dtype, skip, z,
+                    z_stride, dt_bias, dt_softplus, &p.f));
+  if (!dtype_ok(dy_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown dtype of dy %d", fn, dy_dtype);
+  if (!dtype_ok(grad_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown gradient dtype %d", fn, grad_dtype);
+  CHECK(token_array(fn, "dy", dy, dy_stride, D, dy_dtype));
+  REQUIRE(dx && ddt && dB && dC && dA && (dz != nullptr) == (z != nullptr),
+          "%s: dx, ddt, dB, dC and dA must be non-NULL, and dz given exactly when z is", fn);
+  REQUIRE(aligned(dx, 16) && aligned(ddt, 16) && aligned(dB, 16) && aligned(dC, 16) && aligned(dz, 16) &&
+              aligned(dA, 16) && aligned(d_skip, 4) && aligned(d_dt_bias, 4) && aligned(d_state_in, 16) &&
+              aligned(d_state_out, 16) && aligned(chunk_states, 16),
+          "%s: gradients and states must be 16-byte aligned", fn);
+  const void *ins[] = {x, dt, z, Bm, Cm, dy}, *outs[] = {dx, ddt, dz, dB, dC};
+  for (const void *o : outs)
+    for (const void *i : ins) REQUIRE(!o || o != i, "%s: a gradient may not overlap an input", fn);
+  const BackwardSpace w = backward_space(B, T, D, N, G, chunk_states || chunks_of(T) == 0);
+  REQUIRE(workspace && aligned(workspace, 16) && workspace_bytes >= w.total * sizeof(float),
+          "%s: the workspace must be 16-byte aligned and hold %zu bytes (got %zu)", fn, w.total * sizeof(float),
+          workspace_bytes);
+  float *ws = static_cast<float *>(workspace);
+  const hipStream_t hs = static_cast<hipStream_t>(stream);
+  const bool bf16 = in_dtype == WKV_BF16;
+  p.f.n_chunks = chunks_of(T);
+  p.f.chunk_states = const_cast<float *>(chunk_states);
+  if (!chunk_states && p.f.n_chunks > 0) {
+    p.f.chunk_states = ws + w.chunks;
+    wkv::ScanSsmParams states = p.f;  // the forward pass without its output
+    states.nseg = wkv::scan_segments(B, T, (long)B * T, D, N, G, &states.seg_len);
+    states.workspace = ws + w.carry;
+    const hipError_t e = wkv::launch_ssm_scan(states, bf16, hs);
+    if (e != hipSuccess) return launched(e, fn);
+  }
+  p.dy = {dy, (long)dy_stride};
+  p.dy_bf16 = dy_dtype == WKV_BF16;
+  p.d_state_out = d_state_out;
+  p.dx = dx; p.ddt = ddt; p.dz = dz; p.dB = dB; p.dC = dC;
+  p.grad_bf16 = grad_dtype == WKV_BF16;
+  p.dA = dA; p.d_skip = d_skip; p.d_bias = d_dt_bias; p.d_state_in = d_state_in;
+  p.seg_len = w.seg_len; p.nseg = w.nseg;
+  p.carry = ws + w.carry; p.part_A = ws + w.part_A; p.part_ch = ws + w.part_ch; p.part_bc = ws + w.part_bc;
+  return launched(wkv::launch_ssm_scan_backward(p, bf16, hs), fn);
 }
 
 wkv_status wkv_ssm_scan_forward_varlen(int num_slots, int D, int N, int G, const int32_t *lengths, int max_len,

@@ -5,30 +5,10 @@
 // Every (channel, state) has a decay of its own, so nothing here is a matrix product: a token costs
 // D N exponentials (a quarter-rate instruction) and 4 D N multiplies and fused multiply-adds on the
 // vector ALUs, against 8 D bytes of bf16 traffic.  With N = 16 the ALUs bound it.
-#include "ssm_device.hpp"
+#include "ssm_tile.hpp"
 
 namespace wkv {
 namespace {
-
-// Four state values of one channel: values 4q .. 4q + 3 of the N a row holds (zero beyond N).
-__device__ __forceinline__ void load_state4(const float *row, int q, int N, bool whole, float (&h)[4]) {
-  if (whole) {
-    loadv<false>(row, 4 * q, h);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = 4 * q + i < N ? row[4 * q + i] : 0.f;
-  }
-}
-
-__device__ __forceinline__ void store_state4(float *row, int q, int N, bool whole, const float (&h)[4]) {
-  if (whole) {
-    storev<false>(row, 4 * q, h);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * q + i < N) row[4 * q + i] = h[i];
-  }
-}
 
 // LN adjacent lanes share a channel, four states each; the tokens are walked one by one.
 template <bool BF16, int LN>
@@ -81,72 +61,14 @@ __global__ void __launch_bounds__(256) ssm_scan_short_kernel(ScanSsmParams p) {
 //     - delta, delta x - and the widened B and C rows into LDS, and finish the results of the tile
 //     before (skip, gate, rounding) for row-wide stores;
 //   - the scan waves walk the channels: four states of a channel per lane, LN lanes a channel.  The
-//     matrix unit adds the outer product: v_mfma_f32_4x4x1 takes, per block of four lanes, four B
-//     values and four delta x and adds their product to the 4 x 4 decayed states, so that a state
-//     costs a lane two multiplies, an exponential and the multiply-add into y.  (fp32 throughout.)
+//     matrix unit forms the outer product: v_mfma_f32_4x4x1 takes, per block of four lanes, four B
+//     values and four delta x, so that a state costs a lane a multiply, an exponential and two
+//     multiply-adds.  (fp32 throughout; y on the matrix unit as well was slower: 367 us, not 314.)
 //     The partial sums over n are spread over the LN lanes, LN tokens at a time.
 //
 // Few rows: the sequence is cut into nseg segments.  The carry pass runs all but the last from a
 // state of zero and leaves each one's final state and its sum of delta; as the decay over a segment
 // is e^(A sum delta), the main pass folds the earlier segments' states into its own start.
-
-// VW adjacent elements as loaded: widened when they are used, so that no load is waited for early.
-template <bool BF16, bool VEC, int VW>
-struct RawRow {
-  uint32_t w[VEC && BF16 ? (VW + 1) / 2 : VW];
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, const uint32_t (&col)[VEC ? 1 : VW]) {
-    if constexpr (VEC) {
-      if constexpr (sizeof w == 16) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(row + col[0]), 0, 0);
-        w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
-      } else if constexpr (sizeof w == 8) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)(row + col[0]), 0, 0);
-        w[0] = v[0]; w[1] = v[1];
-      } else {
-        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)(row + col[0]), 0, 0);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        if constexpr (BF16) w[e] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)(row + col[e]), 0, 0);
-        else w[e] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)(row + col[e]), 0, 0);
-      }
-    }
-  }
-  // Keeps every use behind this point, so that the wait for the loads stays there.
-  __device__ __forceinline__ void arrive() {
-#pragma unroll
-    for (auto &x : w) asm volatile("" : "+v"(x));
-  }
-  __device__ __forceinline__ float get(int e) const {
-    if constexpr (VEC && BF16) return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
-    else if constexpr (BF16) return bf16_lo(w[e]);
-    else return __uint_as_float(w[e]);
-  }
-};
-
-// VW adjacent results through a window.
-template <bool BF16, bool VEC, int VW>
-__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t row, const uint32_t (&col)[VEC ? 1 : VW], const float (&v)[VW]) {
-  if constexpr (!VEC) {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      if constexpr (BF16) __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(v[e]), r, (int)(row + col[e]), 0, 0);
-      else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), r, (int)(row + col[e]), 0, 0);
-    }
-  } else if constexpr (BF16) {
-    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    if constexpr (VW == 4) __builtin_amdgcn_raw_buffer_store_b64(u2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, r, (int)(row + col[0]), 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(v[0], v[1]), r, (int)(row + col[0]), 0, 0);
-  } else {
-    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-    if constexpr (VW == 4)
-      __builtin_amdgcn_raw_buffer_store_b128(u4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, r,
-                                             (int)(row + col[0]), 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b64(u2{__float_as_uint(v[0]), __float_as_uint(v[1])}, r, (int)(row + col[0]), 0, 0);
-  }
-}
 
 template <int LN>
 struct Tile {
@@ -160,35 +82,8 @@ struct Tile {
   static constexpr int YROW = CH + (LN > 1 ? 64 / LN : 0);  // LN token rows written at once: distinct banks
 };
 
-// v[i] of the LN lanes of a channel (lane bits 2 ..), summed over them: lane q of them returns the sum
-// of v[q].  Each step halves the values: a lane keeps those that its own bit selects.
-template <int LN>
-__device__ __forceinline__ float spread4(const float (&v)[LN], int q) {
-  if constexpr (LN == 1) {
-    return v[0];
-  } else {
-    constexpr int half = LN / 2;
-    float r[half];
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      if constexpr (LN >= 8) {  // the rows of 16 (halves of 32) trade places: one's own and the partner's values meet
-        const uint32_t a = __float_as_uint(v[i]), b = __float_as_uint(v[i + half]);
-        const auto w = LN == 16 ? __builtin_amdgcn_permlane32_swap(a, b, false, false) : __builtin_amdgcn_permlane16_swap(a, b, false, false);
-        r[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
-      } else {
-        constexpr int kDown = LN == 4 ? 0x128 : 0x104, kUp = LN == 4 ? 0x128 : 0x114;  // lane ^ 8 by rotation; lane + 4, lane - 4
-        const float lo = v[i] + dpp<kDown>(v[i]), hi = v[i + half] + dpp<kUp>(v[i + half]);
-        r[i] = q & half ? hi : lo;
-      }
-    }
-    return spread4<half>(r, q);
-  }
-}
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 // What four tokens need of LDS.
-template <int LN, bool CARRY>
+template <int LN, bool OUT>
 struct Quad {
   float2 dx[4];
   float b[4];
@@ -199,27 +94,28 @@ struct Quad {
     for (int u = 0; u < 4; ++u) {
       dx[u] = s_dx[t + u][ch];
       b[u] = s_b[t + u][4 * q + j];
-      if constexpr (!CARRY) c[u] = *reinterpret_cast<const float4 *>(&s_c[t + u][4 * q]);
+      if constexpr (OUT) c[u] = *reinterpret_cast<const float4 *>(&s_c[t + u][4 * q]);
     }
   }
   // One token: the states' update and the lane's part of y.
   __device__ __forceinline__ float step(int u, const float (&A)[4], f32x4 &h) const {
+    const f32x4 xb = __builtin_amdgcn_mfma_f32_4x4x1f32(b[u], dx[u].y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] *= __builtin_amdgcn_exp2f(dx[u].x * A[i]);
-    h = __builtin_amdgcn_mfma_f32_4x4x1f32(b[u], dx[u].y, h, 0, 0, 0);
-    if constexpr (CARRY) return 0.f;
+    for (int i = 0; i < 4; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(dx[u].x * A[i]), h[i], xb[i]);
+    if constexpr (!OUT) return 0.f;
     else return fmaf(c[u].w, h[3], fmaf(c[u].z, h[2], fmaf(c[u].y, h[1], c[u].x * h[0])));
   }
 };
 
-template <bool BF16, bool VEC, int LN, bool CARRY>
+// CARRY: the carry pass.  OUT: whether y is formed; the main pass without it only leaves the chunk states.
+template <bool BF16, bool VEC, int LN, bool CARRY, bool OUT>
 __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(ScanSsmParams p) {
   using T = Tile<LN>;
   constexpr int CH = T::CH, TT = T::TT, VW = T::VW, NI = T::NI, NP = T::NP, NB = T::NB;
   __shared__ __align__(16) float2 s_dx[2][TT][CH];  // delta, delta x
   __shared__ __align__(16) float s_b[2][TT][NP];
-  __shared__ __align__(16) float s_c[CARRY ? 1 : 2][CARRY ? 1 : TT][NP];
-  __shared__ __align__(16) float s_y[CARRY ? 1 : 2][CARRY ? 1 : TT][T::YROW];
+  __shared__ __align__(16) float s_c[OUT ? 2 : 1][OUT ? TT : 1][NP];
+  __shared__ __align__(16) float s_y[OUT ? 2 : 1][OUT ? TT : 1][T::YROW];
 
   const int tid = threadIdx.x & 255;
   const bool scanning = uniform((int)(threadIdx.x >> 8)) == 0;
@@ -270,9 +166,9 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
     f32x4 h = {h0[0], h0[1], h0[2], h0[3]};
     if (tiles > 0) __syncthreads();
     for (int k = 0; k < tiles; ++k) {
-      const int buf = k & 1, cbuf = CARRY ? 0 : buf;
+      const int buf = k & 1, cbuf = OUT ? buf : 0;
       constexpr int S = LN > 8 ? LN : 8;  // LDS reads run four tokens ahead of the arithmetic
-      Quad<LN, CARRY> quad[2];
+      Quad<LN, OUT> quad[2];
       quad[0].load(s_dx[buf], s_b[buf], s_c[cbuf], 0, ch, q, j);
 #pragma unroll 1
       for (int u0 = 0; u0 < TT; u0 += S) {
@@ -285,9 +181,9 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
           for (int u = 0; u < 4; ++u) {
             const float y = quad[(v / 4) & 1].step(u, A, h);
             if constexpr (CARRY) total += quad[(v / 4) & 1].dx[u].x;
-            else part[(LN > 4 ? v : 0) + u] = y;
+            if constexpr (OUT) part[(LN > 4 ? v : 0) + u] = y;
           }
-          if constexpr (!CARRY) {
+          if constexpr (OUT) {
             if constexpr (LN <= 4) {
 #pragma unroll
               for (int w = 0; w < 4; w += LN) {
@@ -304,12 +200,12 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
             }
           }
         }
-      }
-      if constexpr (!CARRY) {
-        const int t = t_begin + (k + 1) * TT;
-        if (p.chunk_states && live && t % kScanChunk == 0 && t < sq.len) {
-          const float out[4] = {h[0], h[1], h[2], h[3]};
-          store_state4(p.chunk_states + (((long)blockIdx.y * p.n_chunks + t / kScanChunk - 1) * p.D + d) * N, q, N, whole, out);
+        if constexpr (!CARRY) {
+          const int t = t_begin + k * TT + u0 + S;
+          if (p.chunk_states && live && t % kScanChunk == 0 && t < sq.len) {
+            const float at_t[4] = {h[0], h[1], h[2], h[3]};
+            store_state4(p.chunk_states + (((long)blockIdx.y * p.n_chunks + t / kScanChunk - 1) * p.D + d) * N, q, N, whole, at_t);
+          }
         }
       }
       __syncthreads();
@@ -347,7 +243,7 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
   Raw x[NI], dt[NI], z[NI];                    // of the tile requested
   Raw x_scan[NI], z_scan[NI], x_done[NI], z_done[NI];  // of the tile being scanned, and of the one before
   uint32_t bb[NB] = {}, cc[NB] = {};
-  const bool gate = !CARRY && p.z.base;
+  const bool gate = OUT && p.z.base;
   const int b_n = tid % NP, b_t = tid / NP;  // B and C: state and token of this thread's first value
   constexpr int B_STEP = 256 / NP;
   const bool b_in = TT * NP >= 256 || b_t < TT;
@@ -377,10 +273,10 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
       const int ob = (int)(t * (uint32_t)p.Bm.stride * EL + b_col), oc = (int)(t * (uint32_t)p.Cm.stride * EL + b_col);
       if constexpr (BF16) {
         bb[i] = __builtin_amdgcn_raw_buffer_load_b16(wb, ob, 0, 0);
-        if constexpr (!CARRY) cc[i] = __builtin_amdgcn_raw_buffer_load_b16(wc, oc, 0, 0);
+        if constexpr (OUT) cc[i] = __builtin_amdgcn_raw_buffer_load_b16(wc, oc, 0, 0);
       } else {
         bb[i] = __builtin_amdgcn_raw_buffer_load_b32(wb, ob, 0, 0);
-        if constexpr (!CARRY) cc[i] = __builtin_amdgcn_raw_buffer_load_b32(wc, oc, 0, 0);
+        if constexpr (OUT) cc[i] = __builtin_amdgcn_raw_buffer_load_b32(wc, oc, 0, 0);
       }
     }
   };
@@ -418,7 +314,7 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
       const int t = (b_t + i * B_STEP) & (TT - 1);
       if (b_in) {
         s_b[buf][t][b_n] = BF16 ? bf16_lo(bb[i]) : __uint_as_float(bb[i]);
-        if constexpr (!CARRY) s_c[buf][t][b_n] = BF16 ? bf16_lo(cc[i]) : __uint_as_float(cc[i]);
+        if constexpr (OUT) s_c[buf][t][b_n] = BF16 ? bf16_lo(cc[i]) : __uint_as_float(cc[i]);
       }
     }
   };
@@ -458,14 +354,14 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
   __syncthreads();
   for (int k = 0; k < tiles; ++k) {
     const int t0 = t_begin + k * TT;
-    if (!CARRY && k) finish(t0 - TT, (k - 1) & 1);
-    if constexpr (!CARRY) {
+    if (OUT && k) finish(t0 - TT, (k - 1) & 1);
+    if constexpr (OUT) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) { x_done[i] = x_scan[i]; z_done[i] = z_scan[i]; }
     }
     if (k + 1 < tiles) {
       stage(t0 + TT, (k + 1) & 1);
-      if constexpr (!CARRY) {
+      if constexpr (OUT) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) { x_scan[i] = x[i]; z_scan[i] = z[i]; }
       }
@@ -473,31 +369,33 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
     }
     __syncthreads();
   }
-  if constexpr (!CARRY) finish(t_begin + (tiles - 1) * TT, (tiles - 1) & 1);
+  if constexpr (OUT) finish(t_begin + (tiles - 1) * TT, (tiles - 1) & 1);
+}
+
+template <bool BF16, int LN, bool CARRY, bool OUT>
+void go_tiles(const ScanSsmParams &p, dim3 grid, bool vec, hipStream_t s) {
+  if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, CARRY, OUT>), grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, CARRY, OUT>), grid, dim3(512), 0, s, p);
 }
 
 template <bool BF16, int LN>
 hipError_t go(const ScanSsmParams &p, hipStream_t s) {
   constexpr int CH = 256 / LN, VW = Tile<LN>::VW;
   const int per_group = p.D / p.G, blocks = p.G * ((per_group + CH - 1) / CH);
-  if (p.seq.T <= kScanShort) {
+  if (p.seq.T <= kScanShort && p.y) {
     hipLaunchKernelGGL((ssm_scan_short_kernel<BF16, LN>), dim3(blocks, p.seq.units), dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  const auto fits = [&](const TokenArray &a) {
-    return !a.base || (a.stride % VW == 0 && reinterpret_cast<uintptr_t>(a.base) % (VW * (BF16 ? 2 : 4)) == 0);
-  };
-  const bool vec = per_group % VW == 0 && fits(p.x) && fits(p.dt) && fits(p.z);
+  const int el = BF16 ? 2 : 4;
+  const bool vec = per_group % VW == 0 && in_steps(p.x, VW, el) && in_steps(p.dt, VW, el) && in_steps(p.z, VW, el);
   if (p.nseg > 1) {
-    const dim3 grid(blocks, p.seq.units, p.nseg - 1);
-    if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, true>), grid, dim3(512), 0, s, p);
-    else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, true>), grid, dim3(512), 0, s, p);
+    go_tiles<BF16, LN, true, false>(p, dim3(blocks, p.seq.units, p.nseg - 1), vec, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const dim3 grid(blocks, p.seq.units, p.nseg);
-  if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, false>), grid, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, false>), grid, dim3(512), 0, s, p);
+  if (p.y) go_tiles<BF16, LN, false, true>(p, grid, vec, s);
+  else go_tiles<BF16, LN, false, false>(p, grid, vec, s);
   return hipGetLastError();
 }
 
@@ -514,17 +412,21 @@ hipError_t by_states(const ScanSsmParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Segments of a call: one where its workgroups fill the chip, else as many as fill it.
-int scan_segments(int units, int T, int D, int N, int G, int *seg_len) {
+// Segments of a call.  A segment's workgroups cost 1.65 passes (the carry pass included) instead of
+// one, so a call is cut only where the rows leave most of the chip idle; total / T stands for the
+// full-length rows of a call whose slots differ.
+int scan_segments(int units, int T, long total, int D, int N, int G, int *seg_len) {
   const int CH = 256 / lanes_of(N);
-  const long groups = (long)units * G * ((D / G + CH - 1) / CH);
   *seg_len = T > 0 ? T : 1;
-  if (T <= kScanSplit || groups >= 192 || groups == 0) return 1;
+  if (T <= kScanSplit || units < 1) return 1;
+  const long full = total / T + 1 < units ? total / T + 1 : units;
+  const long groups = full * G * ((D / G + CH - 1) / CH);
+  if (groups > 160) return 1;
   const int want = (int)(512 / groups) < 32 ? (int)(512 / groups) : 32;
   int len = (T + want - 1) / want;
   len = (len + kScanSplit - 1) / kScanSplit * kScanSplit;
   const int n = (T + len - 1) / len;
-  if (n < 3) return 1;  // the carry pass costs about three quarters of the main one
+  if (n < 3) return 1;
   *seg_len = len;
   return n;
 }

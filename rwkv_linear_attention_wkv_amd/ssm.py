@@ -18,7 +18,8 @@ from . import _native
 from ._marshal import _out_code
 from ._native import check
 
-__all__ = ["ssm_conv_forward", "ssm_conv_forward_varlen", "ssm_scan_forward", "ssm_scan_forward_varlen",
+__all__ = ["ssm_conv_forward", "ssm_conv_backward", "ssm_conv_forward_varlen", "ssm_scan_forward", "ssm_scan_forward_train",
+           "ssm_scan_backward", "ssm_scan_forward_varlen",
            "state_store_alloc", "state_store_write", "state_store_read"]
 
 _lib = _native.load()
@@ -172,6 +173,37 @@ def ssm_conv_forward(x, weight, bias=None, state=None, state_map=None, *, activa
     return y, state_out
 
 
+def ssm_conv_backward(x, weight, bias, dy, state=None, state_map=None, *, activation=None, d_state=None,
+                      return_d_state=True, dev_status=None, grad_dtype=torch.float32):
+    """Gradients of :func:`ssm_conv_forward` (the same inputs, T >= 1).
+
+    ``dy`` [B, T, D] (float32 or bfloat16) is the gradient of y, ``d_state`` [B, W-1, D] fp32 that of the final
+    state.  Returns ``(dx [B, T, D] in grad_dtype, dweight [D, W], dbias [D] or None, d_state_in [B, W-1, D] or
+    None)``, the last three in float32; ``d_state_in[b]`` belongs to the initial state row b started from.
+    """
+    code = _first(x, "x", 3)
+    B, T, D = x.shape
+    _, W, par = _conv_params(x, weight, bias, activation)
+    xa = _rows(x, "x", x.shape[:2], (D,), x)
+    (si, mp, n_state, _), _ = _dense_states(state, state_map, None, False, B, (W - 1, D), x)
+    if not isinstance(dy, torch.Tensor) or dy.dtype not in _CODES:
+        raise TypeError("dy must be a bfloat16 or float32 torch.Tensor")
+    if grad_dtype not in _CODES:
+        raise TypeError(f"unsupported gradient dtype {grad_dtype} (bfloat16 or float32)")
+    dya = _rows(dy, "dy", x.shape[:2], (D,), x, same=False)
+    ds = _flat(d_state, "d_state", torch.float32, torch.Size((B, W - 1, D)), x)
+    f = dict(dtype=torch.float32, device=x.device)
+    dx = torch.empty(x.shape, dtype=grad_dtype, device=x.device)
+    dw = torch.empty((D, W), **f)
+    db = torch.empty((D,), **f) if bias is not None else None
+    d_first = torch.empty((B, W - 1, D), **f) if return_d_state else None
+    need = _lib.wkv_ssm_conv_backward_workspace(B, T, D, W)
+    ws = torch.empty(need // 4, **f)
+    _launch(x, _lib.wkv_ssm_conv_backward, B, T, D, W, *xa, code, *par, *dya, _CODES[dy.dtype], si, mp, n_state, ds,
+            _ptr(dx), _CODES[grad_dtype], _ptr(dw), _ptr(db), _ptr(d_first), _ptr(ws), need, _status(dev_status, x))
+    return dx, dw, db, d_first
+
+
 def ssm_conv_forward_varlen(lengths, x, weight, bias, state, *, max_len, state_out=None, state_map=None,
                             activation=None, y=None, dev_status=None, out_dtype=torch.float32):
     """:func:`ssm_conv_forward` over packed rows of slots; updates ``state_out`` (default: ``state`` in place).
@@ -208,9 +240,9 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code):
                          _flat(dt_bias, "dt_bias", torch.float32, torch.Size((width,)), x), int(bool(dt_softplus)))
 
 
-def _workspace(rows, T, width, N, G, ref):
+def _workspace(rows, T, total, width, N, G, ref):
     """Memory for a scan that is cut into segments, allocated on the current stream for one call, or None; its bytes."""
-    need = _lib.wkv_ssm_scan_workspace(rows, T, width, N, G) if T > 64 else 0
+    need = _lib.wkv_ssm_scan_workspace(rows, T, total, width, N, G) if T > 64 else 0
     return (torch.empty(need // 4, dtype=torch.float32, device=ref.device) if need else None), need
 
 
@@ -230,10 +262,74 @@ def ssm_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, s
     width, N, G, args = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code)
     states, state_out = _dense_states(state, state_map, state_out, return_state, rows, (width, N), x)
     y, oc = _output(y, out_dtype, x.shape, x)
-    ws, ws_bytes = _workspace(rows, T, width, N, G, x)
+    ws, ws_bytes = _workspace(rows, T, rows * T, width, N, G, x)
     _launch(x, _lib.wkv_ssm_scan_forward, rows, T, width, N, G, *args, y.data_ptr(), oc, *states, _ptr(ws), ws_bytes,
             _status(dev_status, x))
     return y, state_out
+
+
+def _chunks(T):
+    return max((T + 15) // 16 - 1, 0)
+
+
+def ssm_scan_forward_train(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, state_map=None, *, dt_softplus=True,
+                           y=None, state_out=None, return_state=True, dev_status=None, out_dtype=torch.float32,
+                           chunk_states=None):
+    """:func:`ssm_scan_forward` that also saves the state at every 16-token boundary for :func:`ssm_scan_backward`.
+
+    Returns ``(y, state_out or None, chunk_states [B, ceil(T/16) - 1, D, N] fp32)``.
+    """
+    code = _first(x, "x", 3)
+    rows, T, _ = x.shape
+    width, N, G, args = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code)
+    states, state_out = _dense_states(state, state_map, state_out, return_state, rows, (width, N), x)
+    y, oc = _output(y, out_dtype, x.shape, x)
+    saved = torch.Size((rows, _chunks(T), width, N))
+    if chunk_states is None:
+        chunk_states = torch.empty(saved, dtype=torch.float32, device=x.device)
+    ws, ws_bytes = _workspace(rows, T, rows * T, width, N, G, x)
+    _launch(x, _lib.wkv_ssm_scan_forward_train, rows, T, width, N, G, *args, y.data_ptr(), oc, *states,
+            _flat(chunk_states, "chunk_states", torch.float32, saved, x) or None, _ptr(ws), ws_bytes, _status(dev_status, x))
+    return y, state_out, chunk_states
+
+
+def ssm_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, state=None, state_map=None, *, dt_softplus=True,
+                      d_state=None, return_d_state=True, chunk_states=None, dev_status=None, grad_dtype=torch.float32):
+    """Gradients of :func:`ssm_scan_forward` (the same inputs, T >= 1).
+
+    ``dy`` [B, T, D] (float32 or bfloat16) is the gradient of y, ``d_state`` [B, D, N] fp32 that of the final
+    state; ``chunk_states`` what :func:`ssm_scan_forward_train` saved for these inputs (without them they are
+    computed first).  Returns ``(dx, ddt, dA, dB, dC, dD, dz, d_dt_bias, d_state_in)``: dx, ddt, dz [B, T, D] and
+    dB, dC (shaped as B and C) in ``grad_dtype``; dA [D, N], dD, d_dt_bias [D] and d_state_in [B, D, N] in
+    float32.  dD, dz and d_dt_bias are None where their input is, d_state_in unless ``return_d_state``;
+    ``d_state_in[b]`` belongs to the initial state row b started from.
+    """
+    code = _first(x, "x", 3)
+    rows, T, _ = x.shape
+    width, N, G, args = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code)
+    (si, mp, n_state, _), _ = _dense_states(state, state_map, None, False, rows, (width, N), x)
+    if not isinstance(dy, torch.Tensor) or dy.dtype not in _CODES:
+        raise TypeError("dy must be a bfloat16 or float32 torch.Tensor")
+    if grad_dtype not in _CODES:
+        raise TypeError(f"unsupported gradient dtype {grad_dtype} (bfloat16 or float32)")
+    dya = _rows(dy, "dy", x.shape[:-1], (width,), x, same=False)
+    chunks = _flat(chunk_states, "chunk_states", torch.float32, torch.Size((rows, _chunks(T), width, N)), x) or None
+    ds = _flat(d_state, "d_state", torch.float32, torch.Size((rows, width, N)), x)
+    g = dict(dtype=grad_dtype, device=x.device)
+    f = dict(dtype=torch.float32, device=x.device)
+    dx, ddt = torch.empty(x.shape, **g), torch.empty(x.shape, **g)
+    dB, dC = torch.empty(B.shape, **g), torch.empty(C.shape, **g)
+    dz = torch.empty(x.shape, **g) if z is not None else None
+    dA = torch.empty((width, N), **f)
+    dD = torch.empty((width,), **f) if D is not None else None
+    db = torch.empty((width,), **f) if dt_bias is not None else None
+    d_first = torch.empty((rows, width, N), **f) if return_d_state else None
+    need = _lib.wkv_ssm_scan_backward_workspace(rows, T, width, N, G, int(chunks is not None or _chunks(T) == 0))
+    ws = torch.empty(need // 4, **f)
+    _launch(x, _lib.wkv_ssm_scan_backward, rows, T, width, N, G, *args, *dya, _CODES[dy.dtype], si, mp, n_state, chunks, ds,
+            _ptr(dx), _ptr(ddt), _ptr(dB), _ptr(dC), _ptr(dz), _CODES[grad_dtype], _ptr(dA), _ptr(dD), _ptr(db),
+            _ptr(d_first), _ptr(ws), need, _status(dev_status, x))
+    return dx, ddt, dA, dB, dC, dD, dz, db, d_first
 
 
 def ssm_scan_forward_varlen(lengths, x, dt, A, B, C, state, *, max_len, D=None, z=None, dt_bias=None, state_out=None,
@@ -248,7 +344,7 @@ def ssm_scan_forward_varlen(lengths, x, dt, A, B, C, state, *, max_len, D=None, 
     width, N, G, args = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, code)
     S, ln, states = _slot_states(lengths, state, state_map, state_out, (width, N), x)
     y, oc = _output(y, out_dtype, x.shape, x)
-    ws, ws_bytes = _workspace(S, int(max_len), width, N, G, x)
+    ws, ws_bytes = _workspace(S, int(max_len), total, width, N, G, x)
     _launch(x, _lib.wkv_ssm_scan_forward_varlen, S, width, N, G, ln, int(max_len), total, *args, y.data_ptr(), oc,
             *states, _ptr(ws), ws_bytes, _status(dev_status, x))
     return y

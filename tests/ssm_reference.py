@@ -82,3 +82,46 @@ def scan(x, dt, A, B, C, skip, z, bias, first, softplus_on=True, absolute=False)
         o = (h * Cd[t]).sum(-1) + sk * x[t]
         y.append(o if gate is None else o * gate[t])
     return torch.stack(y) if y else x.new_zeros(0, D), h
+
+
+def scan_grads(x, dt, A, B, C, skip, z, bias, first, dy, d_last, softplus_on=True):
+    """Gradients of one sequence by automatic differentiation of the definition, and their magnitudes.
+
+    Returns two dicts with x, dt, A, B, C, skip, z, bias, first.  A magnitude is the gradient with every term taken by
+    its absolute value (A is not positive, so that no two terms of a decay's derivative differ in sign).
+    """
+    def run(absolute):
+        pos = (lambda v: None if v is None else v.abs()) if absolute else (lambda v: v)
+        raw = dt if bias is None else dt + bias
+        delta = softplus(raw) if softplus_on else raw
+        leaf = lambda v: None if v is None else v.clone().requires_grad_()  # noqa: E731
+        X, Bl, Cl, S, F = (leaf(pos(v)) for v in (x, B, C, skip, first))
+        Al = leaf(-A.abs() if absolute else A)
+        decay, step = leaf(delta), leaf(pos(delta))
+        gate = leaf(pos(z * torch.sigmoid(z))) if z is not None else None
+        T, D = x.shape
+        per = D // B.shape[1]
+        h, total = F, 0.0
+        w = pos(dy)
+        for t in range(T):
+            h = torch.exp(decay[t][:, None] * Al) * h + (step[t] * X[t])[:, None] * Bl[t].repeat_interleave(per, dim=0)
+            o = (h * Cl[t].repeat_interleave(per, dim=0)).sum(-1) + (S * X[t] if S is not None else 0)
+            total = total + (w[t] * (o * gate[t] if gate is not None else o)).sum()
+        if d_last is not None:
+            total = total + (h * pos(d_last)).sum()
+        leaves = dict(x=X, decay=decay, step=step, A=Al, B=Bl, C=Cl, skip=S, gate=gate, first=F)
+        names = [k for k, v in leaves.items() if v is not None]
+        got = dict(zip(names, torch.autograd.grad(total, [leaves[k] for k in names], allow_unused=True)))
+        got = {k: torch.zeros_like(leaves[k]) if v is None else v for k, v in got.items()}
+        slope = torch.sigmoid(raw) if softplus_on else torch.ones_like(raw)
+        d = got.pop("decay"), got.pop("step")
+        got["dt"] = (pos(d[0]) + d[1]) * slope
+        got["bias"] = got["dt"].sum(0) if bias is not None else None
+        if z is not None:
+            sg = torch.sigmoid(z)
+            # the gate's slope is a sum, sg + sg z (1 - sg): near z = -1.278 its terms cancel, and a rounding of either
+            # (2^-24 of sg) is many roundings of what is left, so the magnitude adds |z|
+            got["z"] = got.pop("gate") * (sg * (1 + pos(z) * (1 - sg)))
+        return got
+
+    return run(False), run(True)

@@ -81,9 +81,10 @@ def test_scan_refusals(lib):
 
 
 def test_scan_workspace(lib):
-    need = lib.wkv_ssm_scan_workspace(1, 4096, 64, 16, 1)
-    assert need > 0 and lib.wkv_ssm_scan_workspace(1, 64, 64, 16, 1) == 0 and lib.wkv_ssm_scan_workspace(64, 4096, 4096, 16, 1) == 0
-    for bad in ((0, 4096, 64, 16, 1), (1, 4096, 64, 0, 1), (1, 4096, 64, 65, 1), (1, 4096, 64, 16, 3), (1, -1, 64, 16, 1)):
+    need = lib.wkv_ssm_scan_workspace(1, 4096, 4096, 64, 16, 1)
+    assert need > 0 and lib.wkv_ssm_scan_workspace(1, 64, 64, 64, 16, 1) == 0 and lib.wkv_ssm_scan_workspace(64, 4096, 64 * 4096, 4096, 16, 1) == 0
+    for bad in ((0, 4096, 4096, 64, 16, 1), (1, 4096, 4096, 64, 0, 1), (1, 4096, 4096, 64, 65, 1), (1, 4096, 4096, 64, 16, 3),
+                (1, -1, 4096, 64, 16, 1), (1, 4096, -1, 64, 16, 1)):
         assert lib.wkv_ssm_scan_workspace(*bad) == 0
     assert scan(lib, B=1, T=4096, ws=P, wb=need - 1) == E and b"workspace" in lib.wkv_last_error()
     assert scan(lib, B=1, T=4096, ws=0x10008, wb=need) == E
@@ -129,3 +130,46 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         wkv.state_store_alloc(1, 64, format=torch.uint8, device="cpu")
     with pytest.raises(TypeError, match="store format"):
         wkv.state_store_write(torch.zeros(2, 64), torch.zeros(2, 1), torch.zeros(2, 64))
+
+
+def conv_back(lib, B=2, T=8, D=64, W=4, x=P, xs=64, dt=1, w=P, b=P, act=1, dy=2 * P, ys=64, yt=0, si=None, sm=None, ns=0, dso=None,
+              dx=3 * P, gt=0, dw=P, db=P, dsi=None, ws=P, wb=None, ds=None):
+    wb = lib.wkv_ssm_conv_backward_workspace(B, T, D, W) if wb is None else wb
+    return lib.wkv_ssm_conv_backward(B, T, D, W, x, xs, dt, w, b, act, dy, ys, yt, si, sm, ns, dso, dx, gt, dw, db, dsi, ws, wb, ds, None)
+
+
+def scan_back(lib, B=2, T=8, D=64, N=16, G=1, x=P, xs=64, d=P, dst=64, A=P, b=P, bs=16, c=P, cs=16, dt=1, sk=P, z=P, zs=64, db=P, sp=1,
+              dy=P, ys=64, yt=0, si=None, sm=None, ns=0, ch=None, dso=None, dx=2 * P, ddt=3 * P, dB=4 * P, dC=5 * P, dz=6 * P, gt=0,
+              dA=P, dsk=P, ddb=P, dsi=None, ws=P, wb=None, ds=None):
+    wb = lib.wkv_ssm_scan_backward_workspace(B, T, D, N, G, int(bool(ch))) if wb is None else wb
+    return lib.wkv_ssm_scan_backward(B, T, D, N, G, x, xs, d, dst, A, b, bs, c, cs, dt, sk, z, zs, db, sp, dy, ys, yt, si, sm, ns, ch,
+                                     dso, dx, ddt, dB, dC, dz, gt, dA, dsk, ddb, dsi, ws, wb, ds, None)
+
+
+@pytest.mark.parametrize("fn", [conv_back, scan_back])
+def test_backward_refusals(lib, fn):
+    for kw in (dict(B=0), dict(T=0), dict(D=0), dict(x=None), dict(xs=10), dict(dy=None), dict(ys=10), dict(dy=MIS), dict(dx=None),
+               dict(dx=0x10008), dict(dx=P), dict(ws=None), dict(ws=0x10008), dict(wb=16), dict(si=P, ns=3), dict(sm=P),
+               dict(dso=0x10008), dict(dsi=0x10008), dict(ds=MIS)):
+        assert fn(lib, **kw) == E, kw
+        assert lib.wkv_last_error()
+    for kw in (dict(dt=5), dict(yt=5), dict(gt=5)):
+        assert fn(lib, **kw) == U, kw
+
+
+def test_scan_backward_refusals(lib):
+    for kw in (dict(dz=None), dict(z=None), dict(dA=None), dict(dB=None), dict(dC=0x50008), dict(ddt=None), dict(dz=P), dict(ch=0x10008),
+               dict(dsk=MIS), dict(ddb=MIS), dict(G=3)):
+        assert scan_back(lib, **kw) == E, kw
+    assert scan_back(lib, N=65, bs=65, cs=65, wb=1 << 30) == U
+    plain, saved = (lib.wkv_ssm_scan_backward_workspace(2, 100, 64, 16, 1, k) for k in (0, 1))
+    assert plain - saved == 2 * 6 * 64 * 16 * 4 and lib.wkv_ssm_scan_backward_workspace(2, 0, 64, 16, 1, 0) == 0
+    assert scan_back(lib, T=100, wb=saved) == E and b"workspace" in lib.wkv_last_error()
+
+
+def test_forward_train_needs_room_for_its_states(lib):
+    args = lambda T, ch: (2, T, 64, 16, 1, P, 64, P, 64, P, P, 16, P, 16, 1, P, P, 64, P, 1, 2 * P, 0, None, None, 0, None, ch, None, 0,  # noqa: E731
+                          None, None)
+    assert lib.wkv_ssm_scan_forward_train(*args(17, None)) == E and b"chunk_states" in lib.wkv_last_error()
+    assert lib.wkv_ssm_scan_forward_train(*args(17, 0x10008)) == E
+    assert lib.wkv_ssm_scan_forward_train(*args(0, None)) == OK

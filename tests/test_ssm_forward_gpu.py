@@ -252,7 +252,7 @@ def test_scan_in_place_state_and_carry(T):
 def test_scan_one_long_row(T, D, N, dtype):
     """A row that is cut into segments, with and without a workspace, and as a slot next to short ones."""
     c = scan_case(1, T, D, N, 0, dtype)
-    assert wkv.library().wkv_ssm_scan_workspace(1, T, D, N, 1) > 0
+    assert wkv.library().wkv_ssm_scan_workspace(1, T, T, D, N, 1) > 0
     st = gpu(c["state"])
     y, last = run_scan(c, st, state_out=st)
     check_scan(c, c["state"], y, last, F32)
