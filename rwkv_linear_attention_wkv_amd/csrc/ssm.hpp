@@ -24,7 +24,7 @@ struct SeqParams {
   int32_t *dev_status;
 };
 
-constexpr long kMaxStride = 1 << 24;  // elements between token rows
+constexpr long kMaxStride = 1 << 22;  // elements between token rows
 
 // A token array: element (token t of the call, column c) at base[t * stride + c].
 struct TokenArray {

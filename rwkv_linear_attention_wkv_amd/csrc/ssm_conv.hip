@@ -5,29 +5,56 @@
 //
 // Bound by memory: one read of x and one write of y.  A lane owns V adjacent channels (one load of
 // up to 16 bytes) and walks a segment of the sequence with the last W - 1 inputs in registers, so
-// that an input is read once but for the W - 1 before each segment.  Lane 0's segment also owns
-// the state: it reads it, and writes the new one, so that a call may update it in place.
-#include "ssm_device.hpp"
+// that an input is read once but for the W - 1 before each segment; loads run U tokens ahead.  The
+// first segment also owns the state: it reads it, and writes the new one, so that a call may update
+// it in place.
+#include "ssm_tile.hpp"
 
 namespace wkv {
 namespace {
 
-template <bool BF16, bool YBF16, int W, int V>
-__global__ void __launch_bounds__(256) ssm_conv_kernel(ConvParams p) {
-  const int lane = threadIdx.x & 63, seg = blockIdx.y;
-  const Sequence q = find_sequence(p.seq, blockIdx.z, lane);
-  const int t0 = seg * p.seg_len;
-  if (!q.ok || (seg && t0 >= q.len)) return;
-  const long c = ((long)blockIdx.x * blockDim.x + threadIdx.x) * V;
-  if (c >= p.D) return;
+constexpr int U = 4;  // tokens of one round of loads
 
-  float w[W][V], bias[V], prev[W - 1][V];
+// The taps and bias of V adjacent channels.
+template <int W, int V>
+__device__ __forceinline__ void load_taps(const ConvParams &p, long c, float (&w)[W][V], float (&bias)[V]) {
+  float flat[V * W];
+  if constexpr (V * W % 4 == 0) {  // c is a multiple of V: a whole number of 16-byte words
+    loadv<false>(p.weight, c * W, flat);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) flat[i] = p.weight[c * W + i];
+  }
 #pragma unroll
   for (int e = 0; e < V; ++e) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = p.weight[(c + e) * W + j];
+    for (int j = 0; j < W; ++j) w[j][e] = flat[e * W + j];
     bias[e] = p.bias ? p.bias[c + e] : 0.f;
   }
+}
+
+template <bool BF16, bool YBF16, int W, int V>
+__global__ void __launch_bounds__(256) ssm_conv_kernel(ConvParams p) {
+  const int lane = threadIdx.x & 63, blocks = gridDim.x / p.nseg, seg = blockIdx.x / blocks;
+  const long c = ((long)(blockIdx.x % blocks) * blockDim.x + threadIdx.x) * V;
+  float w[W][V], bias[V], prev[W - 1][V];
+  if (c < p.D) load_taps(p, c, w, bias);
+  const Sequence q = find_sequence(p.seq, blockIdx.y, lane);
+  const int t0 = seg * p.seg_len, t1 = min(t0 + p.seg_len, q.len);
+  if (!q.ok || (seg && t0 >= q.len)) return;
+  if (c >= p.D) return;
+
+  constexpr int EL = BF16 ? 2 : 4, YEL = YBF16 ? 2 : 4;
+  constexpr bool VEC = V > 1;
+  using Raw = RawRow<BF16, VEC, V>;
+  const auto wx = window<EL>(p.x.base, p.x.stride, q.off + t0, t1 - t0, 0, p.D);
+  const auto wy = window<YEL>(p.y, p.D, q.off + t0, t1 - t0, 0, p.D);
+  const uint32_t col[1] = {(uint32_t)c * EL}, ycol[1] = {(uint32_t)c * YEL};
+  const uint32_t step = (uint32_t)p.x.stride * EL, ystep = (uint32_t)p.D * YEL;
+  Raw x[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) x[u].load(wx, u * step, col);
+
   if (seg == 0) {
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
@@ -59,32 +86,45 @@ __global__ void __launch_bounds__(256) ssm_conv_kernel(ConvParams p) {
     for (int i = 0; i < W - 1; ++i) loadv<BF16>(p.x.base, (q.off + t0 - (W - 1) + i) * p.x.stride + c, prev[i]);
   }
 
-  const int t1 = min(t0 + p.seg_len, q.len);
-  constexpr int U = 4;
-  for (int t = t0; t < t1; t += U) {
-    float x[U][V];
+  for (int t = 0; t < t1 - t0; t += U) {
+    Raw next[U];  // rows past the segment read 0, and their results are not written
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < t1) loadv<BF16>(p.x.base, (q.off + t + u) * p.x.stride + c, x[u]);
+    for (int u = 0; u < U; ++u) next[u].load(wx, (t + U + u) * step, col);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (t + u < t1) {
-        float y[V];
+      float y[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float a = bias[e];
+      for (int e = 0; e < V; ++e) {
+        const float xe = x[u].get(e);
+        float a = bias[e];
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], prev[j][e], a);
-          a = fmaf(w[W - 1][e], x[u][e], a);
-          y[e] = p.silu ? a * sigmoid_f(a) : a;
+        for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], prev[j][e], a);
+        a = fmaf(w[W - 1][e], xe, a);
+        y[e] = p.silu ? a * sigmoid_f(a) : a;
 #pragma unroll
-          for (int j = 0; j < W - 2; ++j) prev[j][e] = prev[j + 1][e];
-          prev[W - 2][e] = x[u][e];
-        }
-        storev<YBF16>(p.y, (q.off + t + u) * p.D + c, y);
+        for (int j = 0; j < W - 2; ++j) prev[j][e] = prev[j + 1][e];
+        prev[W - 2][e] = xe;
       }
+      store_row<YBF16, VEC, V>(wy, (t + u) * ystep, ycol, y);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = next[u];
   }
+}
+
+template <bool BF16, int W, int V>
+hipError_t go(const ConvParams &p, hipStream_t s) {
+  const int lanes = (p.D + V - 1) / V;
+  const int block = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
+  const dim3 grid((unsigned)((long)(lanes + block - 1) / block * p.nseg), p.seq.units);
+  if (p.y_bf16) hipLaunchKernelGGL((ssm_conv_kernel<BF16, true, W, V>), grid, dim3(block), 0, s, p);
+  else hipLaunchKernelGGL((ssm_conv_kernel<BF16, false, W, V>), grid, dim3(block), 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool BF16, int V>
+hipError_t by_width(const ConvParams &p, hipStream_t s) {
+  return p.W == 2 ? go<BF16, 2, V>(p, s) : p.W == 3 ? go<BF16, 3, V>(p, s) : go<BF16, 4, V>(p, s);
 }
 
 // Backward.  With d_t = dy_t act'(pre_t) (0 outside the sequence):
@@ -93,11 +133,11 @@ __global__ void __launch_bounds__(256) ssm_conv_kernel(ConvParams p) {
 // One read of x and dy, one write of dx: a lane walks its segment once with the last W - 1 inputs and d
 // in registers, W - 1 tokens past its end.  The sums over tokens leave one row per segment, which a
 // second kernel adds in order.
-template <bool BF16, int W, int V>
+template <bool BF16, bool DYBF16, int W, int V>
 __global__ void __launch_bounds__(256) ssm_conv_backward_kernel(ConvParams p) {
-  const int lane = threadIdx.x & 63, seg = blockIdx.y;
-  const Sequence q = find_sequence(p.seq, blockIdx.z, lane);
-  const long c = ((long)blockIdx.x * blockDim.x + threadIdx.x) * V;
+  const int lane = threadIdx.x & 63, blocks = gridDim.x / p.nseg, seg = blockIdx.x / blocks;
+  const Sequence q = find_sequence(p.seq, blockIdx.y, lane);
+  const long c = ((long)(blockIdx.x % blocks) * blockDim.x + threadIdx.x) * V;
   if (c >= p.D) return;
   float dw[W + 1][V];
 #pragma unroll
@@ -106,13 +146,22 @@ __global__ void __launch_bounds__(256) ssm_conv_backward_kernel(ConvParams p) {
     for (int e = 0; e < V; ++e) dw[j][e] = 0.f;
   const int t0 = seg * p.seg_len, t1 = min(t0 + p.seg_len, q.len);
   if (q.ok) {
+    constexpr int EL = BF16 ? 2 : 4, DEL = DYBF16 ? 2 : 4;
+    constexpr bool VEC = V > 1;
     float w[W][V], bias[V], x[W][V], d[W][V];  // x, d: tokens t - W + 1 .. t
+    const int end = t1 + W - 1, rows = min(end, q.len) - t0;
+    const auto wx = window<EL>(p.x.base, p.x.stride, q.off + t0, rows, 0, p.D);
+    const auto wd = window<DEL>(p.dy.base, p.dy.stride, q.off + t0, rows, 0, p.D);
+    const uint32_t col[1] = {(uint32_t)c * EL}, dcol[1] = {(uint32_t)c * DEL};
+    const uint32_t step = (uint32_t)p.x.stride * EL, dstep = (uint32_t)p.dy.stride * DEL;
+    RawRow<BF16, VEC, V> rx[U];
+    RawRow<DYBF16, VEC, V> ry[U];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[j][e] = p.weight[(c + e) * W + j];
-      bias[e] = p.bias ? p.bias[c + e] : 0.f;
+    for (int u = 0; u < U; ++u) {
+      rx[u].load(wx, u * step, col);
+      ry[u].load(wd, u * dstep, dcol);
     }
+    load_taps(p, c, w, bias);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
 #pragma unroll
@@ -123,66 +172,61 @@ __global__ void __launch_bounds__(256) ssm_conv_backward_kernel(ConvParams p) {
         else if (p.seq.state_in) loadv<false>(p.seq.state_in, ((long)q.row_in * (W - 1) + t + W - 1) * p.D + c, x[i]);
       }
     }
-    constexpr int U = 4;
-    const int end = t1 + W - 1;
     for (int tb = t0; tb < end; tb += U) {
-      float nx[U][V], ny[U][V];
+      RawRow<BF16, VEC, V> nx[U];  // rows past the sequence or the walk read 0
+      RawRow<DYBF16, VEC, V> ny[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (tb + u < min(end, q.len)) {
-          loadv<BF16>(p.x.base, (q.off + tb + u) * p.x.stride + c, nx[u]);
-          if (p.dy_bf16) loadv<true>(p.dy.base, (q.off + tb + u) * p.dy.stride + c, ny[u]);
-          else loadv<false>(p.dy.base, (q.off + tb + u) * p.dy.stride + c, ny[u]);
-        }
+        nx[u].load(wx, (tb - t0 + U + u) * step, col);
+        ny[u].load(wd, (tb - t0 + U + u) * dstep, dcol);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = tb + u;
-        if (t < end) {
-          const bool in = t < q.len;
-          float g[V];
+        const bool own = t < t1;  // its share of the taps' gradients is this segment's
+        float g[V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < V; ++e) {
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) { x[i][e] = x[i + 1][e]; d[i][e] = d[i + 1][e]; }
-            x[W - 1][e] = in ? nx[u][e] : 0.f;
-            float grad = in ? ny[u][e] : 0.f;
-            if (p.silu) {
-              float a = bias[e];
+          for (int i = 0; i < W - 1; ++i) { x[i][e] = x[i + 1][e]; d[i][e] = d[i + 1][e]; }
+          x[W - 1][e] = rx[u].get(e);
+          float grad = ry[u].get(e);
+          if (p.silu) {
+            float a = bias[e];
 #pragma unroll
-              for (int j = 0; j < W; ++j) a = fmaf(w[j][e], x[j][e], a);
-              const float sg = sigmoid_f(a);
-              grad *= sg * fmaf(a, 1.f - sg, 1.f);
-              grad = in ? grad : 0.f;
-            }
-            d[W - 1][e] = grad;
-            if (t < t1) {
-#pragma unroll
-              for (int j = 0; j < W; ++j) dw[j][e] = fmaf(grad, x[j][e], dw[j][e]);
-              dw[W][e] += grad;
-            }
-            float v = 0.f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) v = fmaf(w[W - 1 - i][e], d[i][e], v);
-            g[e] = v;
+            for (int j = 0; j < W; ++j) a = fmaf(w[j][e], x[j][e], a);
+            const float sg = sigmoid_f(a);
+            grad *= sg * fmaf(a, 1.f - sg, 1.f);
           }
-          const int s = t - (W - 1), last = s - (q.len - (W - 1));  // last >= 0: the input is a row of the final state
-          if (s >= t0 || (seg == 0 && p.d_state_in)) {
-            if (last >= 0 && p.d_state_out) {
-              float more[V];
-              loadv<false>(p.d_state_out, ((long)blockIdx.z * (W - 1) + last) * p.D + c, more);
+          grad = t < q.len ? grad : 0.f;
+          d[W - 1][e] = grad;
+          const float mine = own ? grad : 0.f;
 #pragma unroll
-              for (int e = 0; e < V; ++e) g[e] += more[e];
-            }
-            if (s < 0) storev<false>(p.d_state_in, ((long)blockIdx.z * (W - 1) + s + W - 1) * p.D + c, g);
-            else if (p.y_bf16) storev<true>(p.y, (q.off + s) * p.D + c, g);
-            else storev<false>(p.y, (q.off + s) * p.D + c, g);
+          for (int j = 0; j < W; ++j) dw[j][e] = fmaf(mine, own ? x[j][e] : 0.f, dw[j][e]);
+          dw[W][e] += mine;
+          float v = 0.f;
+#pragma unroll
+          for (int i = 0; i < W; ++i) v = fmaf(w[W - 1 - i][e], d[i][e], v);
+          g[e] = v;
+        }
+        const int s = t - (W - 1), last = s - (q.len - (W - 1));  // last >= 0: the input is a row of the final state
+        if (t < end && (s >= t0 || (seg == 0 && p.d_state_in))) {
+          if (last >= 0 && p.d_state_out) {
+            float more[V];
+            loadv<false>(p.d_state_out, ((long)blockIdx.y * (W - 1) + last) * p.D + c, more);
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] += more[e];
           }
+          if (s < 0) storev<false>(p.d_state_in, ((long)blockIdx.y * (W - 1) + s + W - 1) * p.D + c, g);
+          else if (p.y_bf16) storev<true>(p.y, (q.off + s) * p.D + c, g);
+          else storev<false>(p.y, (q.off + s) * p.D + c, g);
         }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) { rx[u] = nx[u]; ry[u] = ny[u]; }
     }
   }
-  const long row = (long)blockIdx.z * p.nseg + seg;
+  const long row = (long)blockIdx.y * p.nseg + seg;
 #pragma unroll
   for (int j = 0; j <= W; ++j) storev<false>(p.partial, (row * (W + 1) + j) * p.D + c, dw[j]);
 }
@@ -212,7 +256,9 @@ template <bool BF16, int W, int V>
 hipError_t go_backward(const ConvParams &p, hipStream_t s) {
   const int lanes = (p.D + V - 1) / V;
   const int block = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
-  hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, W, V>), dim3((lanes + block - 1) / block, p.nseg, p.seq.units), dim3(block), 0, s, p);
+  const dim3 grid((unsigned)((long)(lanes + block - 1) / block * p.nseg), p.seq.units);
+  if (p.dy_bf16) hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, true, W, V>), grid, dim3(block), 0, s, p);
+  else hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, false, W, V>), grid, dim3(block), 0, s, p);
   hipLaunchKernelGGL(ssm_conv_sum_kernel, dim3((p.D + 15) / 16, W + 1), dim3(256), 0, s, p);
   return hipGetLastError();
 }
@@ -222,47 +268,27 @@ hipError_t backward_by_width(const ConvParams &p, hipStream_t s) {
   return p.W == 2 ? go_backward<BF16, 2, V>(p, s) : p.W == 3 ? go_backward<BF16, 3, V>(p, s) : go_backward<BF16, 4, V>(p, s);
 }
 
-template <bool BF16, int W, int V>
-hipError_t go(const ConvParams &p, hipStream_t s) {
-  const int lanes = (p.D + V - 1) / V;
-  const int block = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
-  const dim3 grid((lanes + block - 1) / block, p.nseg, p.seq.units);
-  if (p.y_bf16) hipLaunchKernelGGL((ssm_conv_kernel<BF16, true, W, V>), grid, dim3(block), 0, s, p);
-  else hipLaunchKernelGGL((ssm_conv_kernel<BF16, false, W, V>), grid, dim3(block), 0, s, p);
-  return hipGetLastError();
-}
-
-template <bool BF16, int V>
-hipError_t by_width(const ConvParams &p, hipStream_t s) {
-  return p.W == 2 ? go<BF16, 2, V>(p, s) : p.W == 3 ? go<BF16, 3, V>(p, s) : go<BF16, 4, V>(p, s);
-}
-
-// Whether V channels at a time stay aligned in every row of the array.
-bool fits(const void *base, long stride, int elem, int V) {
-  return stride % V == 0 && reinterpret_cast<uintptr_t>(base) % (unsigned)(V * elem) == 0;
-}
-
 }  // namespace
 
-// Tokens of one walk.
+// Tokens of one walk: at most 64 (its W - 1 extra rows then cost 5 %), down to 16 until the walks give
+// every SIMD a few waves to switch between.
 int conv_segments(int units, int T, int D, bool backward, int *seg_len) {
+  const long per_row = (long)units * ((D / (backward ? 4 : 8) + 63) / 64);  // waves of one segment of every row
   int len = 64;
-  while ((long)len * 65535 < T) len *= 2;
+  while (len > 16 && per_row * ((T + len - 1) / len) < 4096) len /= 2;
   *seg_len = len;
   return T > 0 ? (T + len - 1) / len : 1;
 }
 
 hipError_t launch_ssm_conv(const ConvParams &p, bool bf16, hipStream_t s) {
-  const int elem = bf16 ? 2 : 4, yel = p.y_bf16 ? 2 : 4;
-  const auto can = [&](int V) { return p.D % V == 0 && fits(p.x.base, p.x.stride, elem, V) && fits(p.y, p.D, yel, V); };
+  const TokenArray y = {p.y, p.D};
+  const auto can = [&](int V) { return p.D % V == 0 && in_steps(p.x, V, bf16 ? 2 : 4) && in_steps(y, V, p.y_bf16 ? 2 : 4); };
   if (bf16) return can(8) ? by_width<true, 8>(p, s) : can(2) ? by_width<true, 2>(p, s) : by_width<true, 1>(p, s);
   return can(4) ? by_width<false, 4>(p, s) : by_width<false, 1>(p, s);
 }
 
 hipError_t launch_ssm_conv_backward(const ConvParams &p, bool bf16, hipStream_t s) {
-  const auto can = [&](int V) {
-    return p.D % V == 0 && fits(p.x.base, p.x.stride, bf16 ? 2 : 4, V) && fits(p.dy.base, p.dy.stride, p.dy_bf16 ? 2 : 4, V);
-  };
+  const auto can = [&](int V) { return p.D % V == 0 && in_steps(p.x, V, bf16 ? 2 : 4) && in_steps(p.dy, V, p.dy_bf16 ? 2 : 4); };
   if (bf16) return can(4) ? backward_by_width<true, 4>(p, s) : backward_by_width<true, 1>(p, s);
   return can(4) ? backward_by_width<false, 4>(p, s) : backward_by_width<false, 1>(p, s);
 }

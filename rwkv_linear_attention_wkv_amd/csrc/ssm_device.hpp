@@ -147,7 +147,7 @@ __device__ __forceinline__ float softplus_f(float v) {
 
 // A window of a token array for buffer loads and stores: `rows` rows from `row` on, columns from c
 // on.  Accesses past its last row read 0 and write nothing; columns that a lane does not have are
-// sent there by adding kOutside to their offset.  Offsets are 32-bit: at most 32 rows, of row strides
+// sent there by adding kOutside to their offset.  Offsets are 32-bit: at most 127 rows, of row strides
 // up to kMaxStride.
 constexpr uint32_t kOutside = 0x80000000u;
 template <int ELEM>

@@ -34,7 +34,7 @@ inline bool in_steps(const TokenArray &a, int V, int elem) {
 // VW adjacent elements as loaded: widened when they are used, so that no load is waited for early.
 template <bool BF16, bool VEC, int VW>
 struct RawRow {
-  static_assert(!VEC || VW == 2 || VW == 4, "whole loads are of 2 or 4 elements");
+  static_assert(!VEC || VW == 2 || VW == 4 || (BF16 && VW == 8), "whole loads are of 4, 8 or 16 bytes");
   uint32_t w[VEC && BF16 ? (VW + 1) / 2 : VW];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, const uint32_t (&col)[VEC ? 1 : VW]) {
     if constexpr (VEC) {
@@ -70,7 +70,7 @@ struct RawRow {
 // VW adjacent results through a window.
 template <bool BF16, bool VEC, int VW>
 __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t row, const uint32_t (&col)[VEC ? 1 : VW], const float (&v)[VW]) {
-  static_assert(!VEC || VW == 2 || VW == 4, "whole stores are of 2 or 4 elements");
+  static_assert(!VEC || VW == 2 || VW == 4 || VW == 8, "whole stores are of 2, 4 or 8 elements");
   if constexpr (!VEC) {
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
@@ -79,12 +79,21 @@ __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t row
     }
   } else if constexpr (BF16) {
     typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    if constexpr (VW == 4) __builtin_amdgcn_raw_buffer_store_b64(u2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, r, (int)(row + col[0]), 0, 0);
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    if constexpr (VW == 8)
+      __builtin_amdgcn_raw_buffer_store_b128(u4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}, r,
+                                             (int)(row + col[0]), 0, 0);
+    else if constexpr (VW == 4) __builtin_amdgcn_raw_buffer_store_b64(u2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, r, (int)(row + col[0]), 0, 0);
     else __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(v[0], v[1]), r, (int)(row + col[0]), 0, 0);
   } else {
     typedef uint32_t u2 __attribute__((ext_vector_type(2)));
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-    if constexpr (VW == 4)
+    if constexpr (VW == 8) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 4)
+        __builtin_amdgcn_raw_buffer_store_b128(u4{__float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3])},
+                                               r, (int)(row + col[0] + 4 * k), 0, 0);
+    } else if constexpr (VW == 4)
       __builtin_amdgcn_raw_buffer_store_b128(u4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, r,
                                              (int)(row + col[0]), 0, 0);
     else __builtin_amdgcn_raw_buffer_store_b64(u2{__float_as_uint(v[0]), __float_as_uint(v[1])}, r, (int)(row + col[0]), 0, 0);
