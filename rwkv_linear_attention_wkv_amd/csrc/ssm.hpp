@@ -58,6 +58,7 @@ struct ScanSsmParams {
   SeqParams seq;
   int D, N, G;
   TokenArray x, dt, z, Bm, Cm;  // z.base may be null
+  bool bc_whole;  // B and C rows in loads of four values (set by the launcher)
   const float *A, *skip, *dt_bias;
   bool softplus;
   void *y;

@@ -231,15 +231,15 @@ __global__ void __launch_bounds__(256) ssm_conv_backward_kernel(ConvParams p) {
   for (int j = 0; j <= W; ++j) storev<false>(p.partial, (row * (W + 1) + j) * p.D + c, dw[j]);
 }
 
-// dweight [D, W] and dbias [D] from the segments' rows [W + 1, D]: 16 threads each add every 16th row,
-// then their sums in order.
-__global__ void __launch_bounds__(256) ssm_conv_sum_kernel(ConvParams p) {
-  __shared__ float s[16][17];
-  const int c = threadIdx.x & 15, k = threadIdx.x >> 4, j = blockIdx.y;
-  const long d = (long)blockIdx.x * 16 + c, rows = (long)p.seq.units * p.nseg;
+// dweight [D, W] and dbias [D] from the segments' rows [W + 1, D]: 16 threads a column each add every 16th row,
+// then their sums in order; 64 columns a workgroup, so that a row is read 256 bytes at a time.
+__global__ void __launch_bounds__(1024) ssm_conv_sum_kernel(ConvParams p) {
+  __shared__ float s[16][64];
+  const int c = threadIdx.x & 63, k = threadIdx.x >> 6, j = blockIdx.y;
+  const long d = (long)blockIdx.x * 64 + c, rows = (long)p.seq.units * p.nseg;
   float a = 0.f;
   if (d < p.D) {
-#pragma unroll 4
+#pragma unroll 8
     for (long r = k; r < rows; r += 16) a += p.partial[(r * (p.W + 1) + j) * p.D + d];
   }
   s[k][c] = a;
@@ -259,7 +259,7 @@ hipError_t go_backward(const ConvParams &p, hipStream_t s) {
   const dim3 grid((unsigned)((long)(lanes + block - 1) / block * p.nseg), p.seq.units);
   if (p.dy_bf16) hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, true, W, V>), grid, dim3(block), 0, s, p);
   else hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, false, W, V>), grid, dim3(block), 0, s, p);
-  hipLaunchKernelGGL(ssm_conv_sum_kernel, dim3((p.D + 15) / 16, W + 1), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(ssm_conv_sum_kernel, dim3((p.D + 63) / 64, W + 1), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
 

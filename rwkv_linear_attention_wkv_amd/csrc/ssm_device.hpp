@@ -7,6 +7,23 @@
 
 namespace wkv {
 
+// The value of the lane that DPP control CTRL selects (every lane of the row is active).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // lane ^1, ^2, ^7, ^15
+
+// The sum of x over the wave, in every lane: four steps within the rows of 16, then the rows' sums.
+__device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kXor1, 0xf, 0xf, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kXor2, 0xf, 0xf, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kHalfMirror, 0xf, 0xf, true);
+  x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kMirror, 0xf, 0xf, true);
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 0) + (uint32_t)__builtin_amdgcn_readlane((int)x, 16) +
+         (uint32_t)__builtin_amdgcn_readlane((int)x, 32) + (uint32_t)__builtin_amdgcn_readlane((int)x, 48);
+}
+
 // One sequence of a call, the same in every lane of the wave that asked for it.
 struct Sequence {
   long off;  // first token row
@@ -36,21 +53,23 @@ __device__ __forceinline__ Sequence find_sequence(const SeqParams &p, int unit, 
   } else {
     const int len = p.lengths[unit];
     const int row = p.state_map ? p.state_map[unit] : unit;
-    long sum = 0;
+    uint32_t lo = 0, hi = 0;  // the sum of the lengths before this slot, of their halves of 16 bits: at most 65535 slots
     bool bad = false, dup = false;
     for (int i = lane; i < p.units; i += 64) {
       const int L = p.lengths[i];
-      if (i < unit) sum += L;
+      if (i < unit) {
+        lo += (uint32_t)L & 0xffffu;
+        hi += (uint32_t)L >> 16;
+      }
       bad |= L < 0 || L > p.T;
       if (p.state_map && i != unit && p.state_map[i] == row) dup = true;
     }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+    const long sum = (long)wave_sum(lo) + ((long)wave_sum(hi) << 16);
     if (__any(bad)) status |= WKV_DEV_BAD_LENGTH;
     if (row < 0 || row >= p.n_state) status |= WKV_DEV_BAD_STATE_MAP;
     if (__any(dup)) status |= WKV_DEV_DUPLICATE_ROW;
     if (!(status & WKV_DEV_BAD_LENGTH) && sum + len > p.total_tokens) status |= WKV_DEV_TOKEN_OVERFLOW;
-    q.off = uniform(sum);
+    q.off = sum;
     q.len = uniform(len);
     q.row_in = q.row_out = uniform(row);
   }
@@ -158,37 +177,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void *base, long 
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-// The value of the lane that DPP control CTRL selects (every lane of the row is active).
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
-}
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // lane ^1, ^2, ^7, ^15
-
-// v[i] of the L adjacent lanes that share a channel, summed over them: lane q (its place among
-// the L) returns the sum of v[q].  Each halving keeps the half of the values that the lane's own
-// bit selects and adds the partner's; the partners of the upper bits are the mirrored lanes,
-// whose lower bits differ too, which later halvings make up for.
-template <int L>
-__device__ __forceinline__ float sum_spread(const float (&v)[L], int q) {
-  if constexpr (L == 1) {
-    return v[0];
-  } else {
-    constexpr int half = L / 2;
-    float r[half];
-    const bool up = q & half;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
-      if constexpr (L == 16) r[i] = keep + dpp<kMirror>(send);
-      else if constexpr (L == 8) r[i] = keep + dpp<kHalfMirror>(send);
-      else if constexpr (L == 4) r[i] = keep + dpp<kXor2>(send);
-      else r[i] = keep + dpp<kXor1>(send);
-    }
-    return sum_spread<half>(r, q);
-  }
-}
 
 // The sum of v over the L adjacent lanes that share a channel, in every one of them.
 template <int L>

@@ -10,13 +10,39 @@
 namespace wkv {
 namespace {
 
-// LN adjacent lanes share a channel, four states each; the tokens are walked one by one.
+// Few tokens (single-token steps): LN adjacent lanes share a channel, four states each, and walk the
+// tokens one by one.  Bound by the states' way in and out, one coalesced load and store of 16 bytes a
+// lane; a token's loads leave together, the first token's with the state's.
+template <bool BF16>
+struct ShortToken {
+  float x, dt, z;
+  float B[4], C[4];
+  __device__ __forceinline__ void load(const ScanSsmParams &p, long row, long d, long bc, int n) {
+    x = load1<BF16>(p.x.base, row * p.x.stride + d);
+    dt = load1<BF16>(p.dt.base, row * p.dt.stride + d);
+    z = p.z.base ? load1<BF16>(p.z.base, row * p.z.stride + d) : 0.f;
+    if (p.bc_whole) {  // every lane's four values are a whole load
+      const long at = bc + (n < p.N ? n : 0);
+      loadv<BF16>(p.Bm.base, row * p.Bm.stride + at, B);
+      loadv<BF16>(p.Cm.base, row * p.Cm.stride + at, C);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long at = bc + (n + i < p.N ? n + i : 0);
+        B[i] = load1<BF16>(p.Bm.base, row * p.Bm.stride + at);
+        C[i] = load1<BF16>(p.Cm.base, row * p.Cm.stride + at);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i >= p.N) B[i] = C[i] = 0.f;
+  }
+};
+
 template <bool BF16, int LN>
 __global__ void __launch_bounds__(256) ssm_scan_short_kernel(ScanSsmParams p) {
   constexpr int CH = 256 / LN;  // channels of a workgroup
   const int lane = threadIdx.x & 63, q = threadIdx.x % LN;
-  const Sequence sq = find_sequence(p.seq, blockIdx.y, lane);
-  if (!sq.ok) return;
   const int per_group = p.D / p.G, blocks = (per_group + CH - 1) / CH;
   const int g = blockIdx.x / blocks, in_group = (blockIdx.x % blocks) * CH + threadIdx.x / LN;
   const bool live = in_group < per_group;
@@ -25,30 +51,28 @@ __global__ void __launch_bounds__(256) ssm_scan_short_kernel(ScanSsmParams p) {
   const bool whole = (N & 3) == 0 && 4 * q < N;
   float A[4], h[4] = {0.f, 0.f, 0.f, 0.f};
   load_state4(p.A + d * N, q, N, whole, A);
+  const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
+  const Sequence sq = find_sequence(p.seq, blockIdx.y, lane);
+  if (!sq.ok) return;
+  if (p.seq.state_in) load_state4(p.seq.state_in + ((long)sq.row_in * p.D + d) * N, q, N, whole, h);
+  ShortToken<BF16> now, next;
+  if (sq.len > 0) now.load(p, sq.off, d, (long)g * N, 4 * q);
 #pragma unroll
   for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
-  if (p.seq.state_in) load_state4(p.seq.state_in + ((long)sq.row_in * p.D + d) * N, q, N, whole, h);
-  const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
   for (int t = 0; t < sq.len; ++t) {
     const long r = sq.off + t;
-    const float x = load1<BF16>(p.x.base, r * p.x.stride + d);
-    const float raw = load1<BF16>(p.dt.base, r * p.dt.stride + d) + bias;
-    const float delta = p.softplus ? softplus_f(raw) : raw, dx = delta * x;
+    if (t + 1 < sq.len) next.load(p, r + 1, d, (long)g * N, 4 * q);
+    const float raw = now.dt + bias, delta = p.softplus ? softplus_f(raw) : raw, dx = delta * now.x;
     float part = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int n = 4 * q + i;
-      const float b = n < N ? load1<BF16>(p.Bm.base, r * p.Bm.stride + g * N + n) : 0.f;
-      const float c = n < N ? load1<BF16>(p.Cm.base, r * p.Cm.stride + g * N + n) : 0.f;
-      h[i] = fmaf(__builtin_amdgcn_exp2f(delta * A[i]), h[i], dx * b);
-      part = fmaf(c, h[i], part);
+      h[i] = fmaf(__builtin_amdgcn_exp2f(delta * A[i]), h[i], dx * now.B[i]);
+      part = fmaf(now.C[i], h[i], part);
     }
-    float y = fmaf(skip, x, sum_all<LN>(part));
-    if (p.z.base) {
-      const float z = load1<BF16>(p.z.base, r * p.z.stride + d);
-      y *= z * sigmoid_f(z);
-    }
+    float y = fmaf(skip, now.x, sum_all<LN>(part));
+    if (p.z.base) y *= now.z * sigmoid_f(now.z);
     if (live && q == 0) store1(p.y, r * p.D + d, p.y_bf16, y);
+    now = next;
   }
   if (live && p.seq.state_out && !(sq.len == 0 && p.seq.state_out == p.seq.state_in))
     store_state4(p.seq.state_out + ((long)sq.row_out * p.D + d) * N, q, N, whole, h);
@@ -431,7 +455,9 @@ int scan_segments(int units, int T, long total, int D, int N, int G, int *seg_le
   return n;
 }
 
-hipError_t launch_ssm_scan(const ScanSsmParams &p, bool bf16, hipStream_t s) {
+hipError_t launch_ssm_scan(const ScanSsmParams &call, bool bf16, hipStream_t s) {
+  ScanSsmParams p = call;
+  p.bc_whole = p.N % 4 == 0 && in_steps(p.Bm, 4, bf16 ? 2 : 4) && in_steps(p.Cm, 4, bf16 ? 2 : 4);
   return bf16 ? by_states<true>(p, s) : by_states<false>(p, s);
 }
 

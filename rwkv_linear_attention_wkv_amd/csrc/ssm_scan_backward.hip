@@ -477,14 +477,15 @@ __global__ void __launch_bounds__(256) ssm_backward_bc_kernel(ScanBackwardParams
   else store1(p.dC, to + n - p.f.N, p.grad_bf16, sum);
 }
 
-// out[c] = sum over r of in[r][c]: each of 16 threads adds every 16th row, then the 16 sums in order.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float *in, float *out, long rows, long cols, long stride) {
-  __shared__ float s[16][17];
-  const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
-  const long col = (long)blockIdx.x * 16 + c;
+// out[c] = sum over r of in[r][c]: each of 16 threads adds every 16th row, then the 16 sums in
+// order; 64 columns a workgroup, so that a row is read 256 bytes at a time.
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *in, float *out, long rows, long cols, long stride) {
+  __shared__ float s[16][64];
+  const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
+  const long col = (long)blockIdx.x * 64 + c;
   float a = 0.f;
   if (col < cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (long r = k; r < rows; r += 16) a += in[r * stride + col];
   }
   s[k][c] = a;
@@ -529,7 +530,7 @@ hipError_t by_states(const ScanBackwardParams &p, hipStream_t s) {
 }
 
 hipError_t sum_rows(const float *in, float *out, long rows, long cols, long stride, hipStream_t s) {
-  hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, s, in, out, rows, cols, stride);
+  hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, in, out, rows, cols, stride);
   return hipGetLastError();
 }
 

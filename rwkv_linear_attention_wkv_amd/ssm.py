@@ -47,9 +47,14 @@ def _ptr(t):
 
 
 def _flat(t, name, dtype, shape, ref):
-    """A contiguous tensor of this dtype and shape on the call's device, or None; its address."""
+    """The address of a contiguous tensor of this dtype and shape on the call's device; None for None."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == ref.get_device() and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -58,13 +63,18 @@ def _flat(t, name, dtype, shape, ref):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != ref.device:
         raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, name, lead, width, ref, same=True):
     """A token array of rows ``width`` wide: its address and the step between its rows, in elements."""
+    cols = width[0] if len(width) == 1 else width[0] * width[1]
+    try:
+        if (t.shape == lead + width and t.get_device() == ref.get_device() and (t.dtype is ref.dtype or not same)
+                and t.is_contiguous()):
+            return t.data_ptr(), cols
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if same and t.dtype != ref.dtype:
@@ -73,10 +83,7 @@ def _rows(t, name, lead, width, ref, same=True):
         raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
     if t.shape != lead + width:
         raise ValueError(f"{name} must have shape {tuple(lead + width)}, got {tuple(t.shape)}")
-    cols = 1
-    for w in width:
-        cols *= w
-    if t.is_contiguous() or t.numel() == 0:
+    if t.numel() == 0:
         return t.data_ptr(), cols
     st, k = t.stride(), len(lead)
     step = 1
@@ -95,12 +102,14 @@ def _rows(t, name, lead, width, ref, same=True):
 
 def _launch(ref, fn, *args):
     """Calls the library with the current stream of the tensors' device, that device being current."""
-    dev = ref.device
-    if dev.index == torch.cuda.current_device():
-        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    dev = ref.get_device()
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        check(status)
 
 
 def _output(y, out_dtype, shape, ref):
