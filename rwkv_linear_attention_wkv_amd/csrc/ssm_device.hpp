@@ -150,8 +150,7 @@ __device__ __forceinline__ float sigmoid_f(float v) { return fast_rcp(1.f + fast
 // ln(1 + e^v) = max(v, 0) + ln(1 + e) with e = e^-|v| in (0, 1].  ln(1 + e) / e is a polynomial of degree
 // 8 (a least-squares fit on [0, 1], reweighted until its relative error was level at 2^-25): no
 // cancellation, so a small step keeps its relative accuracy (under 2^-22 with its own roundings).
-__device__ __forceinline__ float softplus_f(float v) {
-  const float e = __builtin_amdgcn_exp2f(fabsf(v) * -1.4426950408889634f);
+__device__ __forceinline__ float softplus_e(float v, float e) {
   float r = 0.005232690833508968f;
   r = fmaf(r, e, -0.029505230486392975f);
   r = fmaf(r, e, 0.07822594791650772f);
@@ -162,6 +161,17 @@ __device__ __forceinline__ float softplus_f(float v) {
   r = fmaf(r, e, -0.4999949336051941f);
   r = fmaf(r, e, 0.9999999403953552f);
   return fmaf(e, r, fmaxf(v, 0.f));
+}
+
+__device__ __forceinline__ float softplus_f(float v) {
+  return softplus_e(v, __builtin_amdgcn_exp2f(fabsf(v) * -1.4426950408889634f));
+}
+
+// The same with its slope, 1 / (1 + e^-v): 1 or e over 1 + e, as v is positive or not.
+__device__ __forceinline__ float softplus_f(float v, float &slope) {
+  const float e = __builtin_amdgcn_exp2f(fabsf(v) * -1.4426950408889634f);
+  slope = (v >= 0.f ? 1.f : e) * fast_rcp(1.f + e);
+  return softplus_e(v, e);
 }
 
 // A window of a token array for buffer loads and stores: `rows` rows from `row` on, columns from c

@@ -36,15 +36,14 @@ struct BTile {
 // Sums of v[0 .. 7] (dB of four states, dC of four) over the channels of a wave: the lanes that
 // differ from this one in the bits above the LN lanes of a channel (each swap or rotation joins two
 // lanes and halves the values) and in the two lowest bits.  Returns the values left in r and the
-// place of the first among the eight; lanes where `mine` is false hold copies.
+// place of the first among the eight; lanes may hold copies of the same value.
 template <int LN>
-__device__ __forceinline__ void sum_channels(const float (&v)[8], int lane, float (&r)[LN == 16 ? 2 : 1], int &place, bool &mine) {
+__device__ __forceinline__ void sum_channels(const float (&v)[8], int lane, float (&r)[LN == 16 ? 2 : 1], int &place) {
   constexpr int B = LN == 2 ? 3 : LN == 4 ? 2 : LN == 8 ? 1 : 0;  // lane bits above a channel's lanes
   float w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = v[i];
   place = 0;
-  mine = true;
   int n = 8;
 #pragma unroll
   for (int s = 0; s < B; ++s) {
@@ -81,7 +80,6 @@ __device__ __forceinline__ void sum_channels(const float (&v)[8], int lane, floa
       n = half;
     } else {
       w[0] += s ? dpp<kXor2>(w[0]) : dpp<kXor1>(w[0]);
-      mine = mine && !(lane >> s & 1);
     }
   }
 #pragma unroll
@@ -211,12 +209,9 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
           }
           float r[LN == 16 ? 2 : 1];
           int place;
-          bool mine;
-          sum_channels<LN>(v, lane, r, place, mine);
-          if (mine) {
+          sum_channels<LN>(v, lane, r, place);
 #pragma unroll
-            for (int i = 0; i < (LN == 16 ? 2 : 1); ++i) s_bc[buf][wave][u][((place + i) >> 2) * NP + 4 * q + ((place + i) & 3)] = r[i];
-          }
+          for (int i = 0; i < (LN == 16 ? 2 : 1); ++i) s_bc[buf][wave][u][((place + i) >> 2) * NP + 4 * q + ((place + i) & 3)] = r[i];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) h0[i] = next[i];
@@ -255,7 +250,10 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
   using Raw = RawRow<BF16, VEC, VW>;
   using Dy = RawRow<false, VEC, VW>;  // dy as fp32, or bf16 in the first words
   struct Item { Raw x, dt, z; Dy dy; };
-  Item want[NI], scan[NI], done[NI];  // of the tile requested, the tile being walked and the one before
+  Item want[NI];  // as loaded, of the tile requested
+  // What the gradients of a (token, channel) need beside the sums: of the tile being walked and the one before.
+  struct Kept { float x[VW], delta[VW], slope[VW], c[VW], gate[VW]; };
+  Kept scan[NI], done[NI];
   uint32_t bb[NB] = {}, cc[NB] = {};
   const bool gate = f.z.base;
   const int b_n = tid % NP, b_t = tid / NP;
@@ -324,36 +322,39 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(bb[i]), "+v"(cc[i]));
-    float delta[NI][VW], c[NI][VW];
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        delta[i][e] = want[i].dt.get(e) + bias[e];
-        c[i][e] = dy_of(want[i], e);
-      }
-    if (f.softplus) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) delta[i][e] = softplus_f(delta[i][e]);
-    }
-    if (gate) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) c[i][e] *= want[i].z.get(e) * sigmoid_f(want[i].z.get(e));
-    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int t = l_t + i * L_STEP;
-      const bool in = t0 + t < t_end;  // a token past the end leaves states and gradients as they are
+      Kept &k = scan[i];
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        const float v = in ? delta[i][e] : 0.f, x = want[i].x.get(e);
-        s_dx[buf][t][l_c + e] = make_float2(v, v * x);
-        s_dc[buf][t][l_c + e] = c[i][e];
-        if constexpr (!CARRY) d_skip[e] = fmaf(c[i][e], x, d_skip[e]);
+        k.x[e] = want[i].x.get(e);
+        k.delta[e] = want[i].dt.get(e) + bias[e];
+        k.slope[e] = 1.f;
+        k.c[e] = dy_of(want[i], e);
+        k.gate[e] = 0.f;
+      }
+      if (f.softplus) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) k.delta[e] = softplus_f(k.delta[e], k.slope[e]);
+      }
+      if (gate) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          const float z = want[i].z.get(e), sg = sigmoid_f(z), dy = k.c[e], u = z * sg;
+          k.c[e] = dy * u;
+          k.gate[e] = dy * (sg + u * (1.f - sg));
+        }
+      }
+      const int t = l_t + i * L_STEP;
+      const bool in = t0 + t < t_end;  // a token past the end leaves states and gradients as they are
+      float2 *dx = &s_dx[buf][t][l_c];
+      float *dc = &s_dc[buf][t][l_c];
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        if (!in) k.delta[e] = k.slope[e] = 0.f;
+        dx[e] = make_float2(k.delta[e], k.delta[e] * k.x[e]);
+        dc[e] = k.c[e];
+        if constexpr (!CARRY) d_skip[e] = fmaf(k.c[e], k.x[e], d_skip[e]);
       }
     }
 #pragma unroll
@@ -381,27 +382,15 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int t = l_t + i * L_STEP;
-      const bool in = t0 + t < t_end;
+      const Kept &k = done[i];
       float gx[VW], gt[VW], gz[VW];
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        const float x = done[i].x.get(e), raw = done[i].dt.get(e) + bias[e], dy = dy_of(done[i], e);
-        float slope = 1.f, delta = raw, c = dy;
-        if (f.softplus) {
-          delta = softplus_f(raw);
-          slope = sigmoid_f(raw);
-        }
-        const float core = fmaf(skip[e], x, s_out[buf][0][t][l_c + e]);
-        gz[e] = 0.f;
-        if (gate) {
-          const float z = done[i].z.get(e), sg = sigmoid_f(z);
-          gz[e] = dy * core * sg * fmaf(z, 1.f - sg, 1.f);
-          c = dy * z * sg;
-        }
         const float gb = s_out[buf][1][t][l_c + e];
-        gx[e] = fmaf(delta, gb, skip[e] * c);
-        gt[e] = slope * fmaf(x, gb, s_out[buf][2][t][l_c + e] * 0.6931471805599453f);
-        d_bias[e] += in ? gt[e] : 0.f;
+        gz[e] = k.gate[e] * fmaf(skip[e], k.x[e], s_out[buf][0][t][l_c + e]);
+        gx[e] = fmaf(k.delta[e], gb, skip[e] * k.c[e]);
+        gt[e] = k.slope[e] * fmaf(k.x[e], gb, s_out[buf][2][t][l_c + e] * 0.6931471805599453f);
+        d_bias[e] += gt[e];
       }
       write(p.dx, i, t0, gx);
       write(p.ddt, i, t0, gt);
@@ -418,8 +407,6 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
   const int last = t_begin + (tiles - 1) * TT;
   request(last);
   stage(last, 0);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) scan[i] = done[i] = want[i];
   if (tiles > 1) request(last - TT);
   __syncthreads();
   for (int k = 0; k < tiles; ++k) {
@@ -431,10 +418,6 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
     }
     if (k + 1 < tiles) {
       stage(t0 - TT, (k + 1) & 1);
-      if constexpr (!CARRY) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) scan[i] = want[i];
-      }
       if (k + 2 < tiles) request(t0 - 2 * TT);
     }
     __syncthreads();
