@@ -22,6 +22,9 @@ namespace {
 
 constexpr int TT = kScanChunk;  // tokens of a tile
 
+template <int V>
+struct Parity { static constexpr int value = V; };
+
 template <int LN>
 struct BTile {
   static constexpr int CH = 256 / LN;
@@ -251,9 +254,10 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
   using Dy = RawRow<false, VEC, VW>;  // dy as fp32, or bf16 in the first words
   struct Item { Raw x, dt, z; Dy dy; };
   Item want[NI];  // as loaded, of the tile requested
-  // What the gradients of a (token, channel) need beside the sums: of the tile being walked and the one before.
+  // What the gradients of a (token, channel) need beside the sums.  A tile's are overwritten by those of
+  // the second tile after it, staged after it is finished: two sets, by the tile's parity.
   struct Kept { float x[VW], delta[VW], slope[VW], c[VW], gate[VW]; };
-  Kept scan[NI], done[NI];
+  Kept kept[2][NI];
   uint32_t bb[NB] = {}, cc[NB] = {};
   const bool gate = f.z.base;
   const int b_n = tid % NP, b_t = tid / NP;
@@ -314,7 +318,8 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
       }
     }
   };
-  const auto stage = [&](int t0, int buf) {
+  const auto stage = [&](int t0, auto parity) {
+    constexpr int buf = decltype(parity)::value;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       want[i].x.arrive(); want[i].dt.arrive(); want[i].dy.arrive();
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
     for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(bb[i]), "+v"(cc[i]));
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      Kept &k = scan[i];
+      Kept &k = kept[buf][i];
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
         k.x[e] = want[i].x.get(e);
@@ -378,11 +383,12 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
       store_row<false, VEC, VW>(window<4>(to, D, row, rows, d0, c_live), (l_t + i * L_STEP) * (uint32_t)D * 4, at, v);
     }
   };
-  const auto finish = [&](int t0, int buf) {  // the gradients of the tile at t0
+  const auto finish = [&](int t0, auto parity) {  // the gradients of the tile at t0
+    constexpr int buf = decltype(parity)::value;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int t = l_t + i * L_STEP;
-      const Kept &k = done[i];
+      const Kept &k = kept[buf][i];
       float gx[VW], gt[VW], gz[VW];
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
@@ -396,34 +402,43 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
       write(p.ddt, i, t0, gt);
       if (gate) write(p.dz, i, t0, gz);
     }
-    for (int e = tid; e < TT * 2 * N; e += 256) {
-      const int t = e / (2 * N), n = e % (2 * N), at = n < N ? n : NP + n - N;
-      if (t0 + t < t_end)
-        p.part_bc[(((long)block * f.seq.total_tokens + sq.off + t0 + t) * f.G + g) * 2 * N + n] =
-            (s_bc[buf][0][t][at] + s_bc[buf][1][t][at]) + (s_bc[buf][2][t][at] + s_bc[buf][3][t][at]);
+    // dB and dC of the tile's tokens: this block's sums
+    constexpr int COLS = 2 * NP, PER = TT * COLS / 256, STEP = 256 / COLS;
+    const int n = tid % COLS, t = tid / COLS;
+    if (n % NP < N) {
+      float *to = p.part_bc + (((long)block * f.seq.total_tokens + sq.off + t0 + t) * f.G + g) * 2 * N + (n < NP ? n : n - NP + N);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const auto &v = s_bc[buf];
+        const int u = t + i * STEP;
+        if (t0 + u < t_end) to[(long)i * STEP * f.G * 2 * N] = (v[0][u][n] + v[1][u][n]) + (v[2][u][n] + v[3][u][n]);
+      }
     }
   };
 
   const int last = t_begin + (tiles - 1) * TT;
   request(last);
-  stage(last, 0);
+  stage(last, Parity<0>{});
   if (tiles > 1) request(last - TT);
   __syncthreads();
-  for (int k = 0; k < tiles; ++k) {
+  const auto step = [&](int k, auto other) {  // while tile k is walked; other: the parity of the tiles beside it
     const int t0 = last - k * TT;
     if constexpr (!CARRY) {
-      if (k) finish(t0 + TT, (k - 1) & 1);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) done[i] = scan[i];
+      if (k) finish(t0 + TT, other);
     }
     if (k + 1 < tiles) {
-      stage(t0 - TT, (k + 1) & 1);
+      stage(t0 - TT, other);
       if (k + 2 < tiles) request(t0 - 2 * TT);
     }
     __syncthreads();
+  };
+  for (int k = 0; k < tiles; k += 2) {
+    step(k, Parity<1>{});
+    if (k + 1 < tiles) step(k + 1, Parity<0>{});
   }
   if constexpr (!CARRY) {
-    finish(t_begin, (tiles - 1) & 1);
+    if (tiles & 1) finish(t_begin, Parity<0>{});
+    else finish(t_begin, Parity<1>{});
     // the threads that share channels add their sums in the order of their tokens (the scan waves are done with s_dx)
     float2 (*sum)[CH] = s_dx[0];
 #pragma unroll
