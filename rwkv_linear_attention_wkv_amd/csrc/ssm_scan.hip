@@ -264,8 +264,9 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
   uint32_t col[VEC ? 1 : VW];
   columns(EL, col);
   using Raw = RawRow<BF16, VEC, VW>;
-  Raw x[NI], dt[NI], z[NI];                    // of the tile requested
-  Raw x_scan[NI], z_scan[NI], x_done[NI], z_done[NI];  // of the tile being scanned, and of the one before
+  // A tile's x and z are needed until it is finished, when the third tile after it is requested: three
+  // sets, taken in turn.  (dt, B and C are staged before the next request.)
+  Raw x[3][NI], z[3][NI], dt[NI];
   uint32_t bb[NB] = {}, cc[NB] = {};
   const bool gate = OUT && p.z.base;
   const int b_n = tid % NP, b_t = tid / NP;  // B and C: state and token of this thread's first value
@@ -273,7 +274,8 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
   const bool b_in = TT * NP >= 256 || b_t < TT;
   const uint32_t b_col = b_n * EL + (b_n < N && b_in ? 0u : kOutside);
 
-  const auto request = [&](int t0) {  // the loads of the tile at t0
+  const auto request = [&](int t0, auto of) {  // the loads of the tile at t0
+    constexpr int set = decltype(of)::value;
     const long row = sq.off + t0;
     const int rows = min(TT, t_end - t0);
     const auto wx = window<EL>(p.x.base, p.x.stride, row, rows, d0, c_live);
@@ -281,13 +283,13 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const uint32_t t = l_t + i * L_STEP;
-      x[i].load(wx, t * (uint32_t)p.x.stride * EL, col);
+      x[set][i].load(wx, t * (uint32_t)p.x.stride * EL, col);
       dt[i].load(wd, t * (uint32_t)p.dt.stride * EL, col);
     }
     if (gate) {
       const auto wz = window<EL>(p.z.base, p.z.stride, row, rows, d0, c_live);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) z[i].load(wz, (l_t + i * L_STEP) * (uint32_t)p.z.stride * EL, col);
+      for (int i = 0; i < NI; ++i) z[set][i].load(wz, (l_t + i * L_STEP) * (uint32_t)p.z.stride * EL, col);
     }
     const auto wb = window<EL>(p.Bm.base, p.Bm.stride, row, rows, (long)g * N, N);
     const auto wc = window<EL>(p.Cm.base, p.Cm.stride, row, rows, (long)g * N, N);
@@ -304,11 +306,12 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
       }
     }
   };
-  const auto stage = [&](int t0, int buf) {  // delta, delta x, B and C of the requested tile
+  const auto stage = [&](int t0, int buf, auto of) {  // delta, delta x, B and C of the requested tile
+    constexpr int set = decltype(of)::value;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      dt[i].arrive(); x[i].arrive();
-      if (gate) z[i].arrive();
+      dt[i].arrive(); x[set][i].arrive();
+      if (gate) z[set][i].arrive();
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(bb[i]), "+v"(cc[i]));
@@ -323,15 +326,18 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
 #pragma unroll
         for (int e = 0; e < VW; ++e) delta[i][e] = softplus_f(delta[i][e]);
     }
+    if (t0 + TT > t_end) {  // tokens past the end leave the state as it is
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < VW; ++e)
+          if (t0 + l_t + i * L_STEP >= t_end) delta[i][e] = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const bool in = t0 + l_t + i * L_STEP < t_end;  // a token past the end leaves the state as it is
       float2 *row = &s_dx[buf][l_t + i * L_STEP][l_c];
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        const float v = in ? delta[i][e] : 0.f;
-        row[e] = make_float2(v, v * x[i].get(e));
-      }
+      for (int e = 0; e < VW; ++e) row[e] = make_float2(delta[i][e], delta[i][e] * x[set][i].get(e));
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -342,17 +348,18 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
       }
     }
   };
-  const auto finish = [&](int t0, int buf) {  // the results of the tile at t0, from the sums of its scan
+  const auto finish = [&](int t0, int buf, auto of) {  // the results of the tile at t0, from the sums of its scan
+    constexpr int set = decltype(of)::value;
     float y[NI][VW];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < VW; ++e) y[i][e] = fmaf(skip[e], x_done[i].get(e), s_y[buf][l_t + i * L_STEP][l_c + e]);
+      for (int e = 0; e < VW; ++e) y[i][e] = fmaf(skip[e], x[set][i].get(e), s_y[buf][l_t + i * L_STEP][l_c + e]);
     if (gate) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < VW; ++e) y[i][e] *= z_done[i].get(e) * sigmoid_f(z_done[i].get(e));
+        for (int e = 0; e < VW; ++e) y[i][e] *= z[set][i].get(e) * sigmoid_f(z[set][i].get(e));
     }
     const long row = sq.off + t0;
     const int rows = min(TT, t_end - t0);
@@ -370,30 +377,30 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
     }
   };
 
-  request(t_begin);
-  stage(t_begin, 0);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) { x_scan[i] = x_done[i] = x[i]; z_scan[i] = z_done[i] = z[i]; }
-  if (tiles > 1) request(t_begin + TT);
+  request(t_begin, Set<0>{});
+  stage(t_begin, 0, Set<0>{});
+  if (tiles > 1) request(t_begin + TT, Set<1>{});
   __syncthreads();
-  for (int k = 0; k < tiles; ++k) {
-    const int t0 = t_begin + k * TT;
-    if (OUT && k) finish(t0 - TT, (k - 1) & 1);
+  const auto step = [&](int k, auto before, auto after) {  // while tile k is scanned; the sets of the tiles beside it
+    const int t0 = t_begin + k * TT, other = (k + 1) & 1;
     if constexpr (OUT) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) { x_done[i] = x_scan[i]; z_done[i] = z_scan[i]; }
+      if (k) finish(t0 - TT, other, before);
     }
-    if (k + 1 < tiles) {
-      stage(t0 + TT, (k + 1) & 1);
-      if constexpr (OUT) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) { x_scan[i] = x[i]; z_scan[i] = z[i]; }
-      }
-      if (k + 2 < tiles) request(t0 + 2 * TT);
-    }
+    if (k + 1 < tiles) stage(t0 + TT, other, after);
+    if (k + 2 < tiles) request(t0 + 2 * TT, before);
     __syncthreads();
+  };
+  for (int k = 0; k < tiles; k += 3) {
+    step(k, Set<2>{}, Set<1>{});
+    if (k + 1 < tiles) step(k + 1, Set<0>{}, Set<2>{});
+    if (k + 2 < tiles) step(k + 2, Set<1>{}, Set<0>{});
   }
-  if constexpr (OUT) finish(t_begin + (tiles - 1) * TT, (tiles - 1) & 1);
+  if constexpr (OUT) {
+    const int k = tiles - 1;
+    if (k % 3 == 0) finish(t_begin + k * TT, k & 1, Set<0>{});
+    else if (k % 3 == 1) finish(t_begin + k * TT, k & 1, Set<1>{});
+    else finish(t_begin + k * TT, k & 1, Set<2>{});
+  }
 }
 
 template <bool BF16, int LN, bool CARRY, bool OUT>

@@ -22,9 +22,6 @@ namespace {
 
 constexpr int TT = kScanChunk;  // tokens of a tile
 
-template <int V>
-struct Parity { static constexpr int value = V; };
-
 template <int LN>
 struct BTile {
   static constexpr int CH = 256 / LN;
@@ -351,12 +348,14 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
         }
       }
       const int t = l_t + i * L_STEP;
-      const bool in = t0 + t < t_end;  // a token past the end leaves states and gradients as they are
+      if (t0 + TT > t_end && t0 + t >= t_end) {  // a token past the end leaves states and gradients as they are
+#pragma unroll
+        for (int e = 0; e < VW; ++e) k.delta[e] = k.slope[e] = 0.f;
+      }
       float2 *dx = &s_dx[buf][t][l_c];
       float *dc = &s_dc[buf][t][l_c];
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        if (!in) k.delta[e] = k.slope[e] = 0.f;
         dx[e] = make_float2(k.delta[e], k.delta[e] * k.x[e]);
         dc[e] = k.c[e];
         if constexpr (!CARRY) d_skip[e] = fmaf(k.c[e], k.x[e], d_skip[e]);
@@ -418,7 +417,7 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
 
   const int last = t_begin + (tiles - 1) * TT;
   request(last);
-  stage(last, Parity<0>{});
+  stage(last, Set<0>{});
   if (tiles > 1) request(last - TT);
   __syncthreads();
   const auto step = [&](int k, auto other) {  // while tile k is walked; other: the parity of the tiles beside it
@@ -433,12 +432,12 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
     __syncthreads();
   };
   for (int k = 0; k < tiles; k += 2) {
-    step(k, Parity<1>{});
-    if (k + 1 < tiles) step(k + 1, Parity<0>{});
+    step(k, Set<1>{});
+    if (k + 1 < tiles) step(k + 1, Set<0>{});
   }
   if constexpr (!CARRY) {
-    if (tiles & 1) finish(t_begin, Parity<0>{});
-    else finish(t_begin, Parity<1>{});
+    if (tiles & 1) finish(t_begin, Set<0>{});
+    else finish(t_begin, Set<1>{});
     // the threads that share channels add their sums in the order of their tokens (the scan waves are done with s_dx)
     float2 (*sum)[CH] = s_dx[0];
 #pragma unroll

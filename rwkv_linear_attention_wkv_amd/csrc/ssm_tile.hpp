@@ -67,6 +67,10 @@ struct RawRow {
   }
 };
 
+// Which of two or three sets of registers a tile uses, as a type.
+template <int V>
+struct Set { static constexpr int value = V; };
+
 // VW adjacent results through a window.
 template <bool BF16, bool VEC, int VW>
 __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t row, const uint32_t (&col)[VEC ? 1 : VW], const float (&v)[VW]) {
