@@ -58,7 +58,6 @@ struct ScanSsmParams {
   SeqParams seq;
   int D, N, G;
   TokenArray x, dt, z, Bm, Cm;  // z.base may be null
-  bool bc_whole;  // B and C rows in loads of four values (set by the launcher)
   const float *A, *skip, *dt_bias;
   bool softplus;
   void *y;
@@ -73,11 +72,12 @@ struct ScanSsmParams {
 
 constexpr int kScanChunk = 16;  // tokens between saved states
 constexpr int kScanShort = 8;   // calls of at most this many tokens a sequence take the kernel without tiles
-constexpr int kScanSplit = 64;  // a segment is a multiple of this; no shorter sequence is split
+constexpr int kScanSplit = 64;  // no sequence of at most this many tokens is split
 
 // Lanes that share a channel, four states each.
 inline int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
+int best_segments(long groups, int T, int step, double shared, double carry, int start, int *seg_len);
 int scan_segments(int units, int T, long total, int D, int N, int G, int *seg_len);
 hipError_t launch_ssm_scan(const ScanSsmParams &p, bool bf16, hipStream_t s);
 

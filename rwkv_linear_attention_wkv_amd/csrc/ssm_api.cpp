@@ -82,7 +82,7 @@ wkv_status conv_checks(const char *fn, int D, int W, wkv_dtype in_dtype, const f
   if (W < 2 || W > 4) return fail(WKV_ERR_UNSUPPORTED, "%s: W=%d is not supported (2, 3 or 4)", fn, W);
   if (!dtype_ok(in_dtype)) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown input dtype %d", fn, in_dtype);
   if (act != WKV_ACT_NONE && act != WKV_ACT_SILU) return fail(WKV_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, act);
-  REQUIRE(weight && aligned(weight, 16) && aligned(bias, 4), "%s: weight must be given and 16-byte aligned, bias 4-byte aligned", fn);
+  REQUIRE(weight && aligned(weight, 4) && aligned(bias, 4), "%s: weight must be given; weight and bias 4-byte aligned", fn);
   return WKV_OK;
 }
 

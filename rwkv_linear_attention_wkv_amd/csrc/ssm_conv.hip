@@ -19,12 +19,7 @@ constexpr int U = 4;  // tokens of one round of loads
 template <int W, int V>
 __device__ __forceinline__ void load_taps(const ConvParams &p, long c, float (&w)[W][V], float (&bias)[V]) {
   float flat[V * W];
-  if constexpr (V * W % 4 == 0) {  // c is a multiple of V: a whole number of 16-byte words
-    loadv<false>(p.weight, c * W, flat);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V * W; ++i) flat[i] = p.weight[c * W + i];
-  }
+  loadv<false>(p.weight, c * W, flat);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
 #pragma unroll
@@ -33,10 +28,10 @@ __device__ __forceinline__ void load_taps(const ConvParams &p, long c, float (&w
   }
 }
 
+// A lane's V channels from c on (none where c is D or more), of segment seg.
 template <bool BF16, bool YBF16, int W, int V>
-__global__ void __launch_bounds__(256) ssm_conv_kernel(ConvParams p) {
-  const int lane = threadIdx.x & 63, blocks = gridDim.x / p.nseg, seg = blockIdx.x / blocks;
-  const long c = ((long)(blockIdx.x % blocks) * blockDim.x + threadIdx.x) * V;
+__device__ __forceinline__ void conv_walk(const ConvParams &p, int seg, long c) {
+  const int lane = threadIdx.x & 63;
   float w[W][V], bias[V], prev[W - 1][V];
   if (c < p.D) load_taps(p, c, w, bias);
   const Sequence q = find_sequence(p.seq, blockIdx.y, lane);
@@ -112,13 +107,32 @@ __global__ void __launch_bounds__(256) ssm_conv_kernel(ConvParams p) {
   }
 }
 
+// The blocks of one segment: whole ones of V channels a lane, then one for the D % V channels left.
+struct Blocks {
+  int threads, whole, all;
+};
+
+template <int V>
+Blocks blocks_of(int D) {
+  const int lanes = D / V, threads = lanes >= 256 ? 256 : lanes > 0 ? (lanes + 63) / 64 * 64 : 64;
+  const int whole = (lanes + threads - 1) / threads;
+  return {threads, whole, whole + (D % V ? 1 : 0)};
+}
+
+template <bool BF16, bool YBF16, int W, int V>
+__global__ void __launch_bounds__(256) ssm_conv_kernel(ConvParams p) {
+  const int blocks = gridDim.x / p.nseg, seg = blockIdx.x / blocks, block = blockIdx.x % blocks;
+  const long lane = (long)block * blockDim.x + threadIdx.x, lanes = p.D / V;
+  if (V > 1 && p.D % V && block == blocks - 1) conv_walk<BF16, YBF16, W, 1>(p, seg, lanes * V + threadIdx.x);
+  else conv_walk<BF16, YBF16, W, V>(p, seg, lane < lanes ? lane * V : p.D);
+}
+
 template <bool BF16, int W, int V>
 hipError_t go(const ConvParams &p, hipStream_t s) {
-  const int lanes = (p.D + V - 1) / V;
-  const int block = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
-  const dim3 grid((unsigned)((long)(lanes + block - 1) / block * p.nseg), p.seq.units);
-  if (p.y_bf16) hipLaunchKernelGGL((ssm_conv_kernel<BF16, true, W, V>), grid, dim3(block), 0, s, p);
-  else hipLaunchKernelGGL((ssm_conv_kernel<BF16, false, W, V>), grid, dim3(block), 0, s, p);
+  const Blocks b = blocks_of<V>(p.D);
+  const dim3 grid((unsigned)((long)b.all * p.nseg), p.seq.units);
+  if (p.y_bf16) hipLaunchKernelGGL((ssm_conv_kernel<BF16, true, W, V>), grid, dim3(b.threads), 0, s, p);
+  else hipLaunchKernelGGL((ssm_conv_kernel<BF16, false, W, V>), grid, dim3(b.threads), 0, s, p);
   return hipGetLastError();
 }
 
@@ -134,10 +148,8 @@ hipError_t by_width(const ConvParams &p, hipStream_t s) {
 // in registers, W - 1 tokens past its end.  The sums over tokens leave one row per segment, which a
 // second kernel adds in order.
 template <bool BF16, bool DYBF16, int W, int V>
-__global__ void __launch_bounds__(256) ssm_conv_backward_kernel(ConvParams p) {
-  const int lane = threadIdx.x & 63, blocks = gridDim.x / p.nseg, seg = blockIdx.x / blocks;
-  const Sequence q = find_sequence(p.seq, blockIdx.y, lane);
-  const long c = ((long)(blockIdx.x % blocks) * blockDim.x + threadIdx.x) * V;
+__device__ __forceinline__ void conv_walk_back(const ConvParams &p, int seg, long c) {
+  const Sequence q = find_sequence(p.seq, blockIdx.y, threadIdx.x & 63);
   if (c >= p.D) return;
   float dw[W + 1][V];
 #pragma unroll
@@ -231,6 +243,14 @@ __global__ void __launch_bounds__(256) ssm_conv_backward_kernel(ConvParams p) {
   for (int j = 0; j <= W; ++j) storev<false>(p.partial, (row * (W + 1) + j) * p.D + c, dw[j]);
 }
 
+template <bool BF16, bool DYBF16, int W, int V>
+__global__ void __launch_bounds__(256) ssm_conv_backward_kernel(ConvParams p) {
+  const int blocks = gridDim.x / p.nseg, seg = blockIdx.x / blocks, block = blockIdx.x % blocks;
+  const long lane = (long)block * blockDim.x + threadIdx.x, lanes = p.D / V;
+  if (V > 1 && p.D % V && block == blocks - 1) conv_walk_back<BF16, DYBF16, W, 1>(p, seg, lanes * V + threadIdx.x);
+  else conv_walk_back<BF16, DYBF16, W, V>(p, seg, lane < lanes ? lane * V : p.D);
+}
+
 // dweight [D, W] and dbias [D] from the segments' rows [W + 1, D]: 16 threads a column each add every 16th row,
 // then their sums in order; 64 columns a workgroup, so that a row is read 256 bytes at a time.
 __global__ void __launch_bounds__(1024) ssm_conv_sum_kernel(ConvParams p) {
@@ -254,11 +274,10 @@ __global__ void __launch_bounds__(1024) ssm_conv_sum_kernel(ConvParams p) {
 
 template <bool BF16, int W, int V>
 hipError_t go_backward(const ConvParams &p, hipStream_t s) {
-  const int lanes = (p.D + V - 1) / V;
-  const int block = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
-  const dim3 grid((unsigned)((long)(lanes + block - 1) / block * p.nseg), p.seq.units);
-  if (p.dy_bf16) hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, true, W, V>), grid, dim3(block), 0, s, p);
-  else hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, false, W, V>), grid, dim3(block), 0, s, p);
+  const Blocks b = blocks_of<V>(p.D);
+  const dim3 grid((unsigned)((long)b.all * p.nseg), p.seq.units);
+  if (p.dy_bf16) hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, true, W, V>), grid, dim3(b.threads), 0, s, p);
+  else hipLaunchKernelGGL((ssm_conv_backward_kernel<BF16, false, W, V>), grid, dim3(b.threads), 0, s, p);
   hipLaunchKernelGGL(ssm_conv_sum_kernel, dim3((p.D + 63) / 64, W + 1), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
@@ -281,16 +300,11 @@ int conv_segments(int units, int T, int D, bool backward, int *seg_len) {
 }
 
 hipError_t launch_ssm_conv(const ConvParams &p, bool bf16, hipStream_t s) {
-  const TokenArray y = {p.y, p.D};
-  const auto can = [&](int V) { return p.D % V == 0 && in_steps(p.x, V, bf16 ? 2 : 4) && in_steps(y, V, p.y_bf16 ? 2 : 4); };
-  if (bf16) return can(8) ? by_width<true, 8>(p, s) : can(2) ? by_width<true, 2>(p, s) : by_width<true, 1>(p, s);
-  return can(4) ? by_width<false, 4>(p, s) : by_width<false, 1>(p, s);
+  return bf16 ? by_width<true, 8>(p, s) : by_width<false, 4>(p, s);
 }
 
 hipError_t launch_ssm_conv_backward(const ConvParams &p, bool bf16, hipStream_t s) {
-  const auto can = [&](int V) { return p.D % V == 0 && in_steps(p.x, V, bf16 ? 2 : 4) && in_steps(p.dy, V, p.dy_bf16 ? 2 : 4); };
-  if (bf16) return can(4) ? backward_by_width<true, 4>(p, s) : backward_by_width<true, 1>(p, s);
-  return can(4) ? backward_by_width<false, 4>(p, s) : backward_by_width<false, 1>(p, s);
+  return bf16 ? backward_by_width<true, 4>(p, s) : backward_by_width<false, 4>(p, s);
 }
 
 }  // namespace wkv

@@ -78,37 +78,68 @@ __device__ __forceinline__ Sequence find_sequence(const SeqParams &p, int unit, 
   return q;
 }
 
-// V consecutive elements of a token array, widened; the address is aligned to the whole load.
+// The slot whose length is the `rank`-th longest (ties by index), for a whole wave: the slots that take
+// longest are then dispatched first.  Every lane ranks its slots against all others, whose lengths
+// are uniform loads; calls of more slots keep their order.
+constexpr int kRankedSlots = 256;
+__device__ __forceinline__ int slot_by_length(const SeqParams &p, int rank, int lane) {
+  if (!p.lengths || p.units > kRankedSlots) return rank;
+  int slot = 0;
+  for (int first = 0; first < p.units; first += 64) {
+    const int mine = first + lane;
+    const int len = mine < p.units ? p.lengths[mine] : -1;
+    int above = 0;
+    for (int j = 0; j < p.units; ++j) {
+      const int other = p.lengths[j];
+      above += other > len || (other == len && j < mine);
+    }
+    const uint64_t hit = __ballot(mine < p.units && above == rank);
+    if (hit) slot = first + __builtin_ctzll(hit);
+  }
+  return uniform(slot);
+}
+
+// Vectors that need only their element's alignment: the memory unit takes loads and stores of up to 16
+// bytes at any address (the mode that the compiler assumes for this target).
+template <int BYTES>
+struct Words;
+template <> struct Words<2> { typedef uint16_t type; };
+template <> struct Words<4> { typedef uint32_t type __attribute__((aligned(2))); };
+template <> struct Words<8> { typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2))); };
+template <> struct Words<16> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
+
+// V consecutive elements, widened.
 template <bool BF16, int V>
 __device__ __forceinline__ void loadv(const void *base, long idx, float (&out)[V]) {
-  if constexpr (BF16) {
-    const uint16_t *p = static_cast<const uint16_t *>(base) + idx;
-    if constexpr (V == 1) {
-      out[0] = bf16_lo(*p);
-    } else if constexpr (V == 2) {
-      const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-      out[0] = bf16_lo(w); out[1] = bf16_hi(w);
-    } else if constexpr (V == 4) {
-      const uint2 w = *reinterpret_cast<const uint2 *>(p);
-      out[0] = bf16_lo(w.x); out[1] = bf16_hi(w.x); out[2] = bf16_lo(w.y); out[3] = bf16_hi(w.y);
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4 *>(p);
-      out[0] = bf16_lo(w.x); out[1] = bf16_hi(w.x); out[2] = bf16_lo(w.y); out[3] = bf16_hi(w.y);
-      out[4] = bf16_lo(w.z); out[5] = bf16_hi(w.z); out[6] = bf16_lo(w.w); out[7] = bf16_hi(w.w);
+  if constexpr (!BF16 && (V == 3 || V > 4)) {
+#pragma unroll
+    for (int i = 0; i + 4 <= V; i += 4) {
+      float part[4];
+      loadv<false>(base, idx + i, part);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) out[i + k] = part[k];
     }
+#pragma unroll
+    for (int i = V / 4 * 4; i < V; ++i) out[i] = static_cast<const float *>(base)[idx + i];
   } else {
-    const float *p = static_cast<const float *>(base) + idx;
-    if constexpr (V == 1) {
-      out[0] = *p;
-    } else if constexpr (V == 2) {
-      const float2 w = *reinterpret_cast<const float2 *>(p);
-      out[0] = w.x; out[1] = w.y;
+    constexpr int EL = BF16 ? 2 : 4;
+    typedef typename Words<V * EL>::type W;
+    const W w = *reinterpret_cast<const W *>(static_cast<const char *>(base) + idx * EL);
+    if constexpr (BF16 && V == 1) {
+      out[0] = bf16_lo(w);
+    } else if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        uint32_t x;
+        if constexpr (V == 2) x = w;
+        else x = w[i / 2];
+        out[i] = i & 1 ? bf16_hi(x) : bf16_lo(x);
+      }
+    } else if constexpr (V == 1) {
+      out[0] = __uint_as_float(w);
     } else {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const float4 w = *reinterpret_cast<const float4 *>(p + i);
-        out[i] = w.x; out[i + 1] = w.y; out[i + 2] = w.z; out[i + 3] = w.w;
-      }
+      for (int i = 0; i < V; ++i) out[i] = __uint_as_float(w[i]);
     }
   }
 }
@@ -116,23 +147,33 @@ __device__ __forceinline__ void loadv(const void *base, long idx, float (&out)[V
 // V consecutive results, rounded to nearest even when the array is bf16.
 template <bool BF16, int V>
 __device__ __forceinline__ void storev(void *base, long idx, const float (&v)[V]) {
-  if constexpr (BF16) {
-    uint16_t *p = static_cast<uint16_t *>(base) + idx;
-    if constexpr (V == 1) *p = bf16_bits(v[0]);
-    else if constexpr (V == 2) *reinterpret_cast<uint32_t *>(p) = pack_bf16(v[0], v[1]);
-    else if constexpr (V == 4)
-      *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    else
-      *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                                 pack_bf16(v[6], v[7]));
-  } else {
-    float *p = static_cast<float *>(base) + idx;
-    if constexpr (V == 1) *p = v[0];
-    else if constexpr (V == 2) *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
-    else {
+  if constexpr (!BF16 && (V == 3 || V > 4)) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    for (int i = 0; i + 4 <= V; i += 4) {
+      const float part[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+      storev<false>(base, idx + i, part);
     }
+#pragma unroll
+    for (int i = V / 4 * 4; i < V; ++i) static_cast<float *>(base)[idx + i] = v[i];
+  } else {
+    constexpr int EL = BF16 ? 2 : 4;
+    typedef typename Words<V * EL>::type W;
+    W w;
+    if constexpr (BF16 && V == 1) {
+      w = bf16_bits(v[0]);
+    } else if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        if constexpr (V == 2) w = pack_bf16(v[i], v[i + 1]);
+        else w[i / 2] = pack_bf16(v[i], v[i + 1]);
+      }
+    } else if constexpr (V == 1) {
+      w = __float_as_uint(v[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+    }
+    *reinterpret_cast<W *>(static_cast<char *>(base) + idx * EL) = w;
   }
 }
 

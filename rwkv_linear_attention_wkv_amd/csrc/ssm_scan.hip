@@ -21,7 +21,7 @@ struct ShortToken {
     x = load1<BF16>(p.x.base, row * p.x.stride + d);
     dt = load1<BF16>(p.dt.base, row * p.dt.stride + d);
     z = p.z.base ? load1<BF16>(p.z.base, row * p.z.stride + d) : 0.f;
-    if (p.bc_whole) {  // every lane's four values are a whole load
+    if ((p.N & 3) == 0) {  // every lane's four values are a whole load
       const long at = bc + (n < p.N ? n : 0);
       loadv<BF16>(p.Bm.base, row * p.Bm.stride + at, B);
       loadv<BF16>(p.Cm.base, row * p.Cm.stride + at, C);
@@ -132,7 +132,7 @@ struct Quad {
 };
 
 // CARRY: the carry pass.  OUT: whether y is formed; the main pass without it only leaves the chunk states.
-template <bool BF16, bool VEC, int LN, bool CARRY, bool OUT>
+template <bool BF16, Rows ROWS, int LN, bool CARRY, bool OUT>
 __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(ScanSsmParams p) {
   using T = Tile<LN>;
   constexpr int CH = T::CH, TT = T::TT, VW = T::VW, NI = T::NI, NP = T::NP, NB = T::NB;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
 
   const int tid = threadIdx.x & 255;
   const bool scanning = uniform((int)(threadIdx.x >> 8)) == 0;
-  const Sequence sq = find_sequence(p.seq, blockIdx.y, tid & 63);
+  const Sequence sq = find_sequence(p.seq, slot_by_length(p.seq, blockIdx.y, tid & 63), tid & 63);
   if (!sq.ok) return;
   const int seg = blockIdx.z, N = p.N;
   const int t_begin = seg * p.seg_len, t_end = min(t_begin + p.seg_len, sq.len);
@@ -249,7 +249,10 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
   // Staging waves.  Item i of a thread is VW adjacent channels of one token.
   if (tiles == 0 || (CARRY && t_end == sq.len)) return;
   constexpr int ROW = CH / VW, L_STEP = 256 / ROW, EL = BF16 ? 2 : 4;
-  const int l_c = (tid % ROW) * VW, l_t = tid / ROW;
+  constexpr bool VEC = ROWS != Rows::kSingle;
+  int l_c = (tid % ROW) * VW;
+  const int l_t = tid / ROW;
+  if constexpr (ROWS == Rows::kOverlap) l_c = min(l_c, c_live - VW);
   float bias[VW], skip[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
@@ -377,6 +380,12 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
     }
   };
 
+  if constexpr (ROWS == Rows::kOverlap) {  // the columns past the block's channels, which nothing else writes
+    for (int e = tid; e < 2 * TT * (CH - c_live); e += 256) {
+      const int row = e / (CH - c_live), c = c_live + e % (CH - c_live);
+      s_dx[row & 1][row >> 1][c] = make_float2(0.f, 0.f);
+    }
+  }
   request(t_begin, Set<0>{});
   stage(t_begin, 0, Set<0>{});
   if (tiles > 1) request(t_begin + TT, Set<1>{});
@@ -404,9 +413,10 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
 }
 
 template <bool BF16, int LN, bool CARRY, bool OUT>
-void go_tiles(const ScanSsmParams &p, dim3 grid, bool vec, hipStream_t s) {
-  if (vec) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, true, LN, CARRY, OUT>), grid, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, false, LN, CARRY, OUT>), grid, dim3(512), 0, s, p);
+void go_tiles(const ScanSsmParams &p, dim3 grid, Rows rows, hipStream_t s) {
+  if (rows == Rows::kWhole) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, Rows::kWhole, LN, CARRY, OUT>), grid, dim3(512), 0, s, p);
+  else if (rows == Rows::kOverlap) hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, Rows::kOverlap, LN, CARRY, OUT>), grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((ssm_scan_tile_kernel<BF16, Rows::kSingle, LN, CARRY, OUT>), grid, dim3(512), 0, s, p);
 }
 
 template <bool BF16, int LN>
@@ -417,16 +427,15 @@ hipError_t go(const ScanSsmParams &p, hipStream_t s) {
     hipLaunchKernelGGL((ssm_scan_short_kernel<BF16, LN>), dim3(blocks, p.seq.units), dim3(256), 0, s, p);
     return hipGetLastError();
   }
-  const int el = BF16 ? 2 : 4;
-  const bool vec = per_group % VW == 0 && in_steps(p.x, VW, el) && in_steps(p.dt, VW, el) && in_steps(p.z, VW, el);
+  const Rows rows = rows_of<CH, VW>(per_group);
   if (p.nseg > 1) {
-    go_tiles<BF16, LN, true, false>(p, dim3(blocks, p.seq.units, p.nseg - 1), vec, s);
+    go_tiles<BF16, LN, true, false>(p, dim3(blocks, p.seq.units, p.nseg - 1), rows, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const dim3 grid(blocks, p.seq.units, p.nseg);
-  if (p.y) go_tiles<BF16, LN, false, true>(p, grid, vec, s);
-  else go_tiles<BF16, LN, false, false>(p, grid, vec, s);
+  if (p.y) go_tiles<BF16, LN, false, true>(p, grid, rows, s);
+  else go_tiles<BF16, LN, false, false>(p, grid, rows, s);
   return hipGetLastError();
 }
 
@@ -443,28 +452,43 @@ hipError_t by_states(const ScanSsmParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Segments of a call.  A segment's workgroups cost 1.65 passes (the carry pass included) instead of
-// one, so a call is cut only where the rows leave most of the chip idle; total / T stands for the
-// full-length rows of a call whose slots differ.
-int scan_segments(int units, int T, long total, int D, int N, int G, int *seg_len) {
-  const int CH = 256 / lanes_of(N);
+// Segments of a call, by a model of its time in tokens of one workgroup walking alone.  A compute
+// unit that has k workgroups takes `shared` k times as long for a token of each (two at once overlap a
+// little; measured 0.88 forward, and 1 backward, where one fills the unit); the carry pass costs the
+// share `carry` of the main one, and a workgroup's start as well as a launch as much as `start` tokens.  groups: the workgroups of
+// one segment of all rows.
+int best_segments(long groups, int T, int step, double shared, double carry, int start, int *seg_len) {
   *seg_len = T > 0 ? T : 1;
-  if (T <= kScanSplit || units < 1) return 1;
-  const long full = total / T + 1 < units ? total / T + 1 : units;
-  const long groups = full * G * ((D / G + CH - 1) / CH);
-  if (groups > 160) return 1;
-  const int want = (int)(512 / groups) < 32 ? (int)(512 / groups) : 32;
-  int len = (T + want - 1) / want;
-  len = (len + kScanSplit - 1) / kScanSplit * kScanSplit;
-  const int n = (T + len - 1) / len;
-  if (n < 3) return 1;
-  *seg_len = len;
-  return n;
+  if (T <= kScanSplit || groups < 1) return 1;
+  const auto walk = [&](long g, int len) {
+    const long k = (g + 255) / 256;
+    return k <= 1 ? double(len + start) : shared * k * len + (k + 1) / 2 * start;  // two start at once
+  };
+  int best = 1;
+  double least = walk(groups, T);
+  for (int want = 2; want <= 32; ++want) {
+    int len = (T + want - 1) / want;
+    len = (len + step - 1) / step * step;
+    const int n = (T + len - 1) / len;
+    if (n < 2) continue;
+    const double t = walk(groups * n, len) + carry * walk(groups * (n - 1), len) + start;
+    if (t < 0.95 * least) {
+      least = t;
+      best = n;
+      *seg_len = len;
+    }
+  }
+  return best;
 }
 
-hipError_t launch_ssm_scan(const ScanSsmParams &call, bool bf16, hipStream_t s) {
-  ScanSsmParams p = call;
-  p.bc_whole = p.N % 4 == 0 && in_steps(p.Bm, 4, bf16 ? 2 : 4) && in_steps(p.Cm, 4, bf16 ? 2 : 4);
+// total / T stands for the full-length rows of a call whose slots differ.
+int scan_segments(int units, int T, long total, int D, int N, int G, int *seg_len) {
+  const int CH = 256 / lanes_of(N);
+  const long full = T > 0 && total / T + 1 < units ? total / T + 1 : units;
+  return best_segments(full * G * ((D / G + CH - 1) / CH), T, 32, 0.88, 0.7, 64, seg_len);
+}
+
+hipError_t launch_ssm_scan(const ScanSsmParams &p, bool bf16, hipStream_t s) {
   return bf16 ? by_states<true>(p, s) : by_states<false>(p, s);
 }
 

@@ -88,7 +88,7 @@ __device__ __forceinline__ void sum_channels(const float (&v)[8], int lane, floa
 
 // CARRY: only the gradient of the state at the start of each segment but the first, from a gradient
 // of zero at its end, and the segment's sum of delta.
-template <bool BF16, bool VEC, int LN, bool CARRY>
+template <bool BF16, Rows ROWS, int LN, bool CARRY>
 __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardParams p) {
   using T = BTile<LN>;
   constexpr int CH = T::CH, VW = T::VW, NI = T::NI, NP = T::NP, NB = T::NB;
@@ -233,7 +233,10 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
   }
 
   constexpr int ROW = CH / VW, L_STEP = 256 / ROW, EL = BF16 ? 2 : 4;
-  const int l_c = (tid % ROW) * VW, l_t = tid / ROW;
+  constexpr bool VEC = ROWS != Rows::kSingle;
+  int l_c = (tid % ROW) * VW;
+  const int l_t = tid / ROW;
+  if constexpr (ROWS == Rows::kOverlap) l_c = min(l_c, c_live - VW);
   float bias[VW], skip[VW], d_skip[VW] = {}, d_bias[VW] = {};
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
@@ -415,6 +418,13 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
     }
   };
 
+  if constexpr (ROWS == Rows::kOverlap) {  // the columns past the block's channels, which nothing writes, have no share in sums
+    for (int e = tid; e < 2 * TT * (CH - c_live); e += 256) {
+      const int row = e / (CH - c_live), c = c_live + e % (CH - c_live);
+      s_dx[row & 1][row >> 1][c] = make_float2(0.f, 0.f);
+      s_dc[row & 1][row >> 1][c] = 0.f;
+    }
+  }
   const int last = t_begin + (tiles - 1) * TT;
   request(last);
   stage(last, Set<0>{});
@@ -494,22 +504,23 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float *in, float *
   }
 }
 
+template <bool BF16, Rows ROWS, int LN>
+void go_rows(const ScanBackwardParams &p, int blocks, hipStream_t s) {
+  if (p.nseg > 1)
+    hipLaunchKernelGGL((ssm_scan_backward_kernel<BF16, ROWS, LN, true>), dim3(blocks, p.f.seq.units, p.nseg - 1), dim3(512), 0, s, p);
+  hipLaunchKernelGGL((ssm_scan_backward_kernel<BF16, ROWS, LN, false>), dim3(blocks, p.f.seq.units, p.nseg), dim3(512), 0, s, p);
+}
+
 template <bool BF16, int LN>
 hipError_t go(const ScanBackwardParams &p, hipStream_t s) {
   constexpr int CH = 256 / LN, VW = BTile<LN>::VW;
   const int per_group = p.f.D / p.f.G, nb = (per_group + CH - 1) / CH, blocks = p.f.G * nb;
-  const int el = BF16 ? 2 : 4;
-  const bool vec = VW > 1 && per_group % VW == 0 && in_steps(p.f.x, VW, el) && in_steps(p.f.dt, VW, el) && in_steps(p.f.z, VW, el) &&
-                   in_steps(p.dy, VW, p.dy_bf16 ? 2 : 4);
-  constexpr bool kVec = VW > 1;  // one channel a thread: no whole loads
-  if (p.nseg > 1) {
-    const dim3 grid(blocks, p.f.seq.units, p.nseg - 1);
-    if (vec) hipLaunchKernelGGL((ssm_scan_backward_kernel<BF16, kVec, LN, true>), grid, dim3(512), 0, s, p);
-    else hipLaunchKernelGGL((ssm_scan_backward_kernel<BF16, false, LN, true>), grid, dim3(512), 0, s, p);
+  const Rows rows = rows_of<CH, VW>(per_group);
+  if constexpr (VW > 1) {
+    if (rows == Rows::kWhole) go_rows<BF16, Rows::kWhole, LN>(p, blocks, s);
+    else if (rows == Rows::kOverlap) go_rows<BF16, Rows::kOverlap, LN>(p, blocks, s);
   }
-  const dim3 grid(blocks, p.f.seq.units, p.nseg);
-  if (vec) hipLaunchKernelGGL((ssm_scan_backward_kernel<BF16, kVec, LN, false>), grid, dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((ssm_scan_backward_kernel<BF16, false, LN, false>), grid, dim3(512), 0, s, p);
+  if (rows == Rows::kSingle) go_rows<BF16, Rows::kSingle, LN>(p, blocks, s);
   const long values = p.f.seq.total_tokens * 2 * p.f.G * p.f.N;
   hipLaunchKernelGGL(ssm_backward_bc_kernel, dim3((unsigned)((values + 255) / 256)), dim3(256), 0, s, p, nb);
   return hipGetLastError();
@@ -539,7 +550,7 @@ int backward_blocks(int D, int N, int G) {
 }
 
 int backward_segments(int units, int T, int D, int N, int G, int *seg_len) {
-  return scan_segments(units, T, (long)units * T, D, N < 5 ? 5 : N, G, seg_len);
+  return best_segments((long)units * G * backward_blocks(D, N, G), T, TT, 1.0, 0.3, 30, seg_len);
 }
 
 hipError_t launch_sum_rows(const float *in, float *out, long rows, long cols, hipStream_t s) {

@@ -26,9 +26,18 @@ __device__ __forceinline__ void store_state4(float *row, int q, int N, bool whol
   }
 }
 
-// Whether loads of V elements at a time stay aligned in every row of the array.
-inline bool in_steps(const TokenArray &a, int V, int elem) {
-  return !a.base || (a.stride % V == 0 && reinterpret_cast<uintptr_t>(a.base) % (unsigned)(V * elem) == 0);
+// How a tile's rows are read and written VW channels at a time.  Whole: the blocks of channels divide
+// by VW (addresses need no alignment: see Words).  Overlap: they do not; the last thread of a block's
+// row moves back onto its neighbour's channels, which both then hold alike.  Single: a block has fewer
+// than VW channels; one by one.
+enum class Rows { kWhole, kOverlap, kSingle };
+
+template <int CH, int VW>
+Rows rows_of(int per_group) {
+  if (VW == 1) return Rows::kSingle;
+  if (per_group % VW == 0) return Rows::kWhole;
+  const int last = (per_group - 1) % CH + 1;  // channels of the last block
+  return last >= VW ? Rows::kOverlap : Rows::kSingle;
 }
 
 // VW adjacent elements as loaded: widened when they are used, so that no load is waited for early.
