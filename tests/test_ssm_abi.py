@@ -108,7 +108,7 @@ def test_store_refusals(lib, name):
 def test_row_steps_of_views():
     """The step between the rows of token arrays, and the views that have none."""
     t = torch.zeros(3, 5, 40)
-    step = lambda v, inner: ssm._rows(v, "x", v.shape[:v.dim() - len(inner)], inner, v)[1]  # noqa: E731
+    step = lambda v, inner: ssm._row_step(v, "x", v.dim() - len(inner))  # noqa: E731
     assert step(t, (40,)) == 40 and step(t[..., 8:24], (16,)) == 40 and step(t[:, :, ::40], (1,)) == 40
     assert step(t[:1, 1:4, :8], (8,)) == 40 and step(t[:, :1, :8], (8,)) == 200 and step(t[0, :, 4:9], (5,)) == 40
     assert step(t[:1, :1, :8], (8,)) == 8 and step(t[..., :12].unflatten(-1, (3, 4)), (3, 4)) == 40
@@ -130,6 +130,8 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         wkv.state_store_alloc(1, 64, format=torch.uint8, device="cpu")
     with pytest.raises(TypeError, match="store format"):
         wkv.state_store_write(torch.zeros(2, 64), torch.zeros(2, 1), torch.zeros(2, 64))
+    with pytest.raises(ValueError, match="device tensor"):
+        wkv.state_store_write(torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2, 1), torch.zeros(2, 64))
 
 
 def conv_back(lib, B=2, T=8, D=64, W=4, x=P, xs=64, dt=1, w=P, b=P, act=1, dy=2 * P, ys=64, yt=0, si=None, sm=None, ns=0, dso=None,
