@@ -400,13 +400,14 @@ def test_dense_state_map_errors():
 # --------------------------------------------------------------------------------------------------- the store
 
 def store_ref(x, fmt):
-    """Codes as numbers, and scales, of rows [R, E]: both quotients in fp32, to nearest."""
+    """Codes as numbers, and scales, of rows [R, E]: both quotients in fp32, to nearest; a group with an infinity or NaN
+    has the scale NaN and codes of 0."""
     R, E = x.shape
     top = 127.0 if fmt == torch.int8 else 448.0
     codes, scales = [], []
     for c in range(0, E, 64):
         part = x[:, c:c + 64]
-        scale = part.abs().amax(1) / top
+        scale = torch.where(torch.isfinite(part).all(1), part.abs().amax(1) / top, torch.nan)
         q = torch.where(scale[:, None] > 0, part / scale[:, None], torch.zeros_like(part)).clamp(-top, top)
         codes.append(q.round() if fmt == torch.int8 else q.to(torch.float8_e4m3fn).float())
         scales.append(scale)
@@ -440,6 +441,28 @@ def test_store_write_and_read(fmt, R, E):
     step = 0.5 * wants.repeat_interleave(64, 1)[:, :E][perm.long()].double() if fmt == torch.int8 else torch.maximum(
         x.double().abs() * 2.0 ** -4, wants.repeat_interleave(64, 1)[:, :E][perm.long()].double() * 2.0 ** -10)
     assert ((full[perm.long()].double() - x.double()).abs() <= step + 4 * 2.0 ** -24 * x.double().abs()).all()
+
+
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+def test_store_quotients_are_correctly_rounded(fmt):
+    """Codes and scales bitwise those of the rounded quotients: a million values, scales of every binary exponent,
+    mantissas of all ones, values next to the border between two codes, and the smallest numbers."""
+    top = 127.0 if fmt == torch.int8 else 448.0
+    exponent = torch.arange(-140, 120, dtype=torch.float64).repeat_interleave(64)  # one group each
+    groups = exponent.numel()
+    x = (draw(8, groups, 64).double() * 2.0 ** exponent[:, None]).float()
+    ones = torch.tensor([0x3fffffff], dtype=torch.int32).view(F32)  # a scale whose mantissa is all ones
+    x[::7, 0] = (ones.double() * top * 2.0 ** exponent[::7]).float()
+    scale = x.abs().amax(1) / top
+    border = (torch.randint(-126, 126, (groups, 16), generator=torch.Generator().manual_seed(9)) + 0.5) * scale[:, None]
+    x[:, 16:32] = torch.where(border.abs() <= x[:, :1].abs(), border, x[:, 16:32])
+    x[:, 32:36] = torch.nextafter(x[:, 16:20], torch.zeros(groups, 4))
+    x = x.reshape(4, -1)
+    data, scales = wkv.state_store_alloc(4, x.shape[1], format=fmt)
+    wkv.state_store_write(data, scales, gpu(x))
+    codes, want = store_ref(x, fmt)
+    # (the largest exponents overflow to infinities: groups that are not numbers)
+    assert torch.equal(scales.cpu().nan_to_num(-1.0), want.nan_to_num(-1.0)) and torch.equal(data.cpu().float(), codes)
 
 
 def test_store_of_states_by_rows():
