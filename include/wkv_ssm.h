@@ -120,7 +120,8 @@ WKV_API size_t wkv_ssm_scan_workspace(int rows, int T, int64_t total_tokens, int
  *              matter and which no other call may use until this one is done; NULL:
  *              the sequences are not cut (slower where they are few and long)
  * A token whose delta is 0 (dt = -inf under the softplus) leaves the state as
- * it is, so rows may be padded on either side that way.
+ * it is, also where A is an infinity, so rows may be padded on either side that
+ * way (with any finite x and B).
  */
 WKV_API wkv_status wkv_ssm_scan_forward(int B, int T, int D, int N, int G,
                         const void *x, int64_t x_stride, const void *dt, int64_t dt_stride,

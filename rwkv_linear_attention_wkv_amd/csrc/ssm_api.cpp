@@ -11,12 +11,14 @@ namespace {
 
 constexpr int kMaxChannels = wkv::kMaxStride;
 constexpr int kMaxStates = 64;
+constexpr int kMaxTokens = 1 << 30;  // of one sequence
 
 // Sequences and states of a dense call; `state_row` floats per state row.
 wkv_status dense_seq(const char *fn, int B, int T, const float *state_in, const int32_t *state_map, int n_state,
                      float *state_out, int32_t *dev_status, wkv::SeqParams *out) {
   REQUIRE(B >= 1 && T >= 0, "%s: need B >= 1 and T >= 0 (got B=%d T=%d)", fn, B, T);
   REQUIRE(B <= kMaxGridY, "%s: B=%d exceeds %d", fn, B, kMaxGridY);
+  REQUIRE(T <= kMaxTokens, "%s: T=%d exceeds %d", fn, T, kMaxTokens);
   if (state_in) {
     REQUIRE(aligned(state_in, 16), "%s: state_in must be 16-byte aligned", fn);
     REQUIRE(n_state >= 1, "%s: n_state must be >= 1 when state_in is given (got %d)", fn, n_state);
@@ -43,6 +45,7 @@ wkv_status varlen_seq(const char *fn, int num_slots, const int32_t *lengths, int
                       int32_t *dev_status, wkv::SeqParams *out) {
   REQUIRE(num_slots >= 0 && max_len >= 0 && total_tokens >= 0,
           "%s: need num_slots >= 0, max_len >= 0, total_tokens >= 0", fn);
+  REQUIRE(max_len <= kMaxTokens, "%s: max_len=%d exceeds %d", fn, max_len, kMaxTokens);
   REQUIRE(num_slots <= kMaxGridY, "%s: num_slots=%d exceeds %d", fn, num_slots, kMaxGridY);
   if (num_slots > 0) {
     REQUIRE(lengths && aligned(lengths, 4), "%s: lengths must be a non-NULL, 4-byte aligned device array", fn);

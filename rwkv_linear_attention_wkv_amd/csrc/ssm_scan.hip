@@ -50,15 +50,13 @@ __global__ void __launch_bounds__(256) ssm_scan_short_kernel(ScanSsmParams p) {
   const int N = p.N;
   const bool whole = (N & 3) == 0 && 4 * q < N;
   float A[4], h[4] = {0.f, 0.f, 0.f, 0.f};
-  load_state4(p.A + d * N, q, N, whole, A);
+  load_decay4(p.A + d * N, q, N, whole, A);
   const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
   const Sequence sq = find_sequence(p.seq, blockIdx.y, lane);
   if (!sq.ok) return;
   if (p.seq.state_in) load_state4(p.seq.state_in + ((long)sq.row_in * p.D + d) * N, q, N, whole, h);
   ShortToken<BF16> now, next;
   if (sq.len > 0) now.load(p, sq.off, d, (long)g * N, 4 * q);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
   for (int t = 0; t < sq.len; ++t) {
     const long r = sq.off + t;
     if (t + 1 < sq.len) next.load(p, r + 1, d, (long)g * N, 4 * q);
@@ -161,9 +159,7 @@ __global__ void __launch_bounds__(512, LN <= 4 ? 4 : 2) ssm_scan_tile_kernel(Sca
     const long d = d0 + (live ? ch : 0);
     const bool whole = (N & 3) == 0 && 4 * q < N;
     float A[4], h0[4] = {0.f, 0.f, 0.f, 0.f}, total = 0.f;
-    load_state4(p.A + d * N, q, N, whole, A);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+    load_decay4(p.A + d * N, q, N, whole, A);
 
     const long slot = (long)p.D * N;  // workspace: [units][nseg][D][N] states, then [units][nseg - 1][D] sums
     float *ws_h = p.workspace + (long)blockIdx.y * p.nseg * slot + d * N;

@@ -127,9 +127,7 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
     const long d = d0 + (live ? ch : 0);
     const bool whole = (N & 3) == 0 && 4 * q < N;
     float A[4], g0[4] = {0.f, 0.f, 0.f, 0.f};
-    load_state4(f.A + d * N, q, N, whole, A);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+    load_decay4(f.A + d * N, q, N, whole, A);
     const long slot = (long)D * N;
     float *carry = p.carry + (long)unit * p.nseg * slot + d * N;
     float *sums = p.carry + (long)f.seq.units * p.nseg * slot + (long)unit * p.nseg * D + d;

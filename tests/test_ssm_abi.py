@@ -49,7 +49,7 @@ def scan_slots(lib, S=2, D=64, N=16, G=1, ln=P, ml=8, tt=16, x=P, xs=64, d=P, ds
 
 @pytest.mark.parametrize("fn", [conv, scan])
 def test_dense_refusals(lib, fn):
-    for kw in (dict(B=0), dict(T=-1), dict(B=70000), dict(D=0), dict(D=1 << 25), dict(x=None), dict(x=ODD), dict(xs=63),
+    for kw in (dict(B=0), dict(T=-1), dict(T=(1 << 30) + 1), dict(B=70000), dict(D=0), dict(D=1 << 25), dict(x=None), dict(x=ODD), dict(xs=63),
                dict(y=None), dict(y=0x10008), dict(y=P), dict(si=0x10008, ns=1), dict(si=P, ns=0), dict(si=P, ns=3), dict(sm=P),
                dict(si=P, sm=MIS, ns=3), dict(si=P, so=P, ns=1), dict(si=P, so=P, sm=P, ns=2), dict(so=0x10008), dict(ds=MIS)):
         assert fn(lib, **kw) == E, kw
@@ -60,7 +60,7 @@ def test_dense_refusals(lib, fn):
 
 @pytest.mark.parametrize("fn", [conv_slots, scan_slots])
 def test_varlen_refusals(lib, fn):
-    for kw in (dict(S=-1), dict(S=70000), dict(ml=-1), dict(tt=-1), dict(ln=None), dict(ln=MIS), dict(si=None), dict(so=None),
+    for kw in (dict(S=-1), dict(S=70000), dict(ml=-1), dict(ml=(1 << 30) + 1), dict(tt=-1), dict(ln=None), dict(ln=MIS), dict(si=None), dict(so=None),
                dict(si=0x10008), dict(ns=0), dict(ns=1), dict(sm=MIS), dict(x=None), dict(y=None), dict(ds=MIS)):
         assert fn(lib, **kw) == E, kw
     assert fn(lib, S=0) == OK

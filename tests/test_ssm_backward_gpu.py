@@ -167,6 +167,22 @@ def test_scan_backward_without_options(z, skip, bias, sp):
     check_scan_grads(c, dy, None, got, softplus_on=sp)
 
 
+@pytest.mark.parametrize("D,G", [(65, 1), (67, 1), (70, 1), (130, 2)])
+def test_scan_backward_channels_of_part_blocks(D, G):
+    """The last block of channels of a group with 1, 3, 6 and 1 of its 64: their sums hold nothing else."""
+    c = scan_case(1, 20, D, 16, G, F32)
+    dy, ds = draw(11, 1, 20, D), draw(12, 1, D, 16)
+    check_scan_grads(c, dy, ds, scan_back(c, dy, ds))
+
+
+@pytest.mark.parametrize("D", [1, 3, 5, 9, 261])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_conv_backward_any_channel_count(D, dtype):
+    c = conv_case(2, 33, D, 4, dtype)
+    dy, ds = draw(7, 2, 33, D, dtype=dtype), draw(8, 2, 3, D)
+    check_conv_grads(c, dy, ds, "silu", conv_back(c, dy, ds, "silu", grad_dtype=dtype), grad=dtype)
+
+
 @pytest.mark.parametrize("T,D,N,dtype", [(300, 70, 16, F32), (450, 40, 32, BF16), (333, 24, 7, F32)])
 def test_scan_backward_across_segments(T, D, N, dtype):
     """Rows that are cut into segments, in both passes."""

@@ -84,6 +84,16 @@ def test_conv_in_place_state_and_carry(T):
     assert torch.equal(torch.cat(parts, 1), whole) and torch.equal(st, last)
 
 
+@pytest.mark.parametrize("D", [1, 3, 5, 8, 9, 2051])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_conv_any_channel_count_in_place(D, dtype):
+    """Channels past the last whole load, in their own block: rows and states of every count, updated in place."""
+    c = conv_case(2, 33, D, 4, dtype)
+    st = gpu(c["state"])
+    y, last = wkv.ssm_conv_forward(gpu(c["x"]), gpu(c["weight"]), gpu(c["bias"]), st, activation="silu", state_out=st, out_dtype=dtype)
+    check_conv(c["x"], c["weight"], c["bias"], c["state"], "silu", y, last, dtype)
+
+
 def test_conv_state_map_and_shared_state():
     c = conv_case(3, 10, 40, 3, F32, n_state=5)
     rows = torch.tensor([4, 0, 4], dtype=torch.int32)
@@ -297,6 +307,36 @@ def test_scan_rows_of_wider_arrays(dtype, lo, T):
     check_scan(c, c["state"], y, last, F32)
 
 
+@pytest.mark.parametrize("D,G", [(65, 1), (67, 1), (70, 1), (130, 2), (198, 3)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scan_channels_of_part_blocks(D, G, dtype):
+    """The last block of channels of a group with 1, 3, 6, 1 and 2 of its 64: single, overlapping and whole rows."""
+    c = scan_case(1, 40, D, 16, G, dtype)
+    y, last = run_scan(c, c["state"])
+    check_scan(c, c["state"], y, last, F32)
+
+
+@pytest.mark.parametrize("S", [65, 300])
+def test_scan_varlen_many_slots(S):
+    """More slots than a wave has lanes, and more than are ranked by length."""
+    r = torch.Generator().manual_seed(S)
+    lengths = torch.randint(0, 40, (S,), generator=r).to(torch.int32)
+    total, D, N = int(lengths.sum()), 12, 8
+    c = scan_case(0, 0, D, N, 0, F32, lead=(total,), n_state=S)
+    st, status = gpu(c["state"]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = wkv.ssm_scan_forward_varlen(gpu(lengths), *(gpu(c[k]) for k in ("x", "dt", "A", "B", "C")), st, max_len=40, D=gpu(c["D"]),
+                                    z=gpu(c["z"]), dt_bias=gpu(c["dt_bias"]), dev_status=status)
+    assert int(status) == 0
+    off = 0
+    for s, n in enumerate(lengths.tolist()):
+        at = slice(off, off + n)
+        want, wl = scan_ref(c, c["state"][s], at)
+        mag, ml = scan_ref(c, c["state"][s], at, absolute=True)
+        assert_within(y[at], want, allowed(mag, scan_roundings(n)), f"slot {s}")
+        assert_within(st[s], wl, allowed(ml, scan_roundings(n)), f"state {s}")
+        off += n
+
+
 def test_scan_padding_by_a_step_of_zero():
     """Tokens with dt = -inf leave the state bitwise as it is, on either side of a row."""
     c = scan_case(1, 40, 32, 16, 0, F32)
@@ -319,6 +359,51 @@ def test_scan_strong_and_zero_decays():
     c["dt"] = c["dt"] * 4 - 8
     y, last = run_scan(c, c["state"])
     check_scan(c, c["state"], y, last, F32)
+
+
+@pytest.mark.parametrize("T", [3, 35])
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(F32).min])
+def test_scan_decays_to_nothing(T, low):
+    """A of minus infinity or the lowest number: a state is its last token's input; tokens past the end, and steps of
+    zero, change nothing."""
+    c = scan_case(2, T, 20, 16, 0, F32)
+    c["A"][:, ::2] = low
+    y, last = run_scan(c, c["state"])
+    check_scan(c, c["state"], y, last, F32)
+    c["dt"][:, -1] = float("-inf")
+    short = {k: v[:, :-1].contiguous() if k in ("x", "dt", "B", "C", "z") else v for k, v in c.items()}
+    _, last = run_scan(c, c["state"])
+    _, before = run_scan(short, c["state"])
+    assert torch.equal(last, before)
+
+
+def test_nothing_leaks_between_slots_and_channels():
+    """NaN and infinities in one slot's tokens and state, and in one channel of another, stay there."""
+    lengths, D, N = [40, 9, 70, 3], 24, 16
+    total = sum(lengths)
+    c = scan_case(0, 0, D, N, 0, F32, lead=(total,), n_state=4)
+    ln = gpu(torch.tensor(lengths, dtype=torch.int32))
+    rest = dict(max_len=70, D=gpu(c["D"]), dt_bias=gpu(c["dt_bias"]))
+
+    def run(c):
+        st, cs = gpu(c["state"].clone()), gpu(draw(7, 4, 3, D))
+        y = wkv.ssm_scan_forward_varlen(ln, *(gpu(c[k]) for k in ("x", "dt", "A", "B", "C")), st, z=gpu(c["z"]), **rest)
+        u = wkv.ssm_conv_forward_varlen(ln, gpu(c["x"]), gpu(draw(8, D, 4)), None, cs, max_len=70, activation="silu")
+        return [t.cpu() for t in (y, st, u, cs)]
+
+    clean = run(c)
+    bad = {k: v.clone() if v is not None else None for k, v in c.items()}
+    bad["x"][40:49], bad["dt"][40:49], bad["B"][40:49], bad["C"][40:49], bad["z"][40:49] = (float(v) for v in ("nan", "inf", "nan", "inf", "-inf"))
+    bad["state"][1] = float("inf")
+    bad["x"][49:119, 5] = float("nan")  # channel 5 of slot 2
+    got = run(bad)
+    rows = torch.ones(total, D, dtype=torch.bool)
+    rows[40:49] = rows[49:119, 5] = False
+    slots = torch.ones(4, D, dtype=torch.bool)
+    slots[1] = slots[2, 5] = False
+    assert torch.equal(got[0][rows], clean[0][rows]) and torch.equal(got[2][rows], clean[2][rows])
+    assert torch.equal(got[1][slots], clean[1][slots])
+    assert torch.equal(got[3].transpose(1, 2)[slots], clean[3].transpose(1, 2)[slots])
 
 
 @pytest.mark.parametrize("lengths", LENGTHS)
