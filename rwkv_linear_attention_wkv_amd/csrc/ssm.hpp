@@ -94,8 +94,7 @@ struct ScanBackwardParams {
   // workspace
   float *carry;     // [B][nseg][D][N] states' gradients at the start of a segment from one of zero at
                     // its end, then [B][nseg][D] sums of delta
-  float *part_A;    // [B * nseg][D][N]
-  float *part_ch;   // [B * nseg][2][D]: d_skip, d_bias
+  float *part;      // [B * nseg][D * N + 2 * D]: a segment's shares of dA, d_skip and d_bias
   float *part_bc;   // [blocks of a group][B * T][G][2 N]: dB, dC of one block of channels
 };
 
@@ -117,8 +116,5 @@ struct StoreParams {
 
 hipError_t launch_store_write(const StoreParams &p, hipStream_t s);
 hipError_t launch_store_read(const StoreParams &p, hipStream_t s);
-
-// out[c] = sum over r of in[r][c], rows in order within each of 16 strided parts.
-hipError_t launch_sum_rows(const float *in, float *out, long rows, long cols, hipStream_t s);
 
 }  // namespace wkv

@@ -121,7 +121,7 @@ int chunks_of(int T) { return T > 0 ? (T + wkv::kScanChunk - 1) / wkv::kScanChun
 
 // The backward pass's workspace, in floats from its start; each part starts at a multiple of four.
 struct BackwardSpace {
-  size_t carry, part_A, part_ch, part_bc, chunks, total;
+  size_t carry, part, part_bc, chunks, total;
   int nseg, seg_len;
 };
 
@@ -142,8 +142,7 @@ BackwardSpace backward_space(int B, int T, int D, int N, int G, bool with_chunks
     if (fwd > carry) carry = fwd;
   }
   w.carry = take(carry);
-  w.part_A = take(parts * row);
-  w.part_ch = take(parts * 2 * D);
+  w.part = take(parts * (row + 2 * D));
   w.part_bc = take((size_t)wkv::backward_blocks(D, N, G) * B * T * G * 2 * N);
   w.chunks = take(with_chunks ? 0 : (size_t)B * chunks_of(T) * row);
   w.total = at;
@@ -395,7 +394,7 @@ wkv_status wkv_ssm_scan_backward(int B, int T, int D, int N, int G, const void *
   p.grad_bf16 = grad_dtype == WKV_BF16;
   p.dA = dA; p.d_skip = d_skip; p.d_bias = d_dt_bias; p.d_state_in = d_state_in;
   p.seg_len = w.seg_len; p.nseg = w.nseg;
-  p.carry = ws + w.carry; p.part_A = ws + w.part_A; p.part_ch = ws + w.part_ch; p.part_bc = ws + w.part_bc;
+  p.carry = ws + w.carry; p.part = ws + w.part; p.part_bc = ws + w.part_bc;
   return launched(wkv::launch_ssm_scan_backward(p, bf16, hs), fn);
 }
 

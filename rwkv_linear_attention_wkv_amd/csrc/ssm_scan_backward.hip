@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
   const long d0 = (long)g * per_group + c_base;
   const int c_live = min(CH, per_group - c_base);
   const int tiles = (t_end - t_begin + TT - 1) / TT;  // at least one
-  const long part = (long)unit * p.nseg + seg;
+  float *shares = p.part + ((long)unit * p.nseg + seg) * D * (N + 2);  // of dA, then d_skip and d_bias
   const Sequence sq = find_sequence(f.seq, unit, tid & 63);
   if (!sq.ok) {  // a rejected row has no share in the parameters' gradients
     if (!CARRY) {
-      for (long i = threadIdx.x; i < (long)c_live * N; i += 512) p.part_A[(part * D + d0) * N + i] = 0.f;
-      for (int i = threadIdx.x; i < c_live; i += 512) p.part_ch[part * 2 * D + d0 + i] = p.part_ch[(part * 2 + 1) * D + d0 + i] = 0.f;
+      for (long i = threadIdx.x; i < (long)c_live * N; i += 512) shares[d0 * N + i] = 0.f;
+      for (int i = threadIdx.x; i < c_live; i += 512) shares[(long)D * N + d0 + i] = shares[(long)D * N + D + d0 + i] = 0.f;
     }
     return;
   }
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
       }
     } else if (live) {
       if (seg == 0 && p.d_state_in) store_state4(p.d_state_in + ((long)unit * D + d) * N, q, N, whole, out);
-      store_state4(p.part_A + (part * D + d) * N, q, N, whole, dA);
+      store_state4(shares + d * N, q, N, whole, dA);
     }
     if constexpr (!CARRY) __syncthreads();  // the staging waves' last sums
     return;
@@ -457,48 +457,53 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
         a += sum[i][tid].x;
         b += sum[i][tid].y;
       }
-      p.part_ch[part * 2 * D + d0 + tid] = a;
-      p.part_ch[(part * 2 + 1) * D + d0 + tid] = b;
+      shares[(long)D * N + d0 + tid] = a;
+      shares[(long)D * N + D + d0 + tid] = b;
     }
   }
 }
 
-// dB and dC: the blocks' sums, added in their order.
-__global__ void __launch_bounds__(256) ssm_backward_bc_kernel(ScanBackwardParams p, int blocks) {
-  const long GN = (long)p.f.G * p.f.N, total = p.f.seq.total_tokens * 2 * GN;
-  const long at = (long)blockIdx.x * 256 + threadIdx.x;
-  if (at >= total) return;
-  const int n = (int)(at % (2 * p.f.N));
-  const long row = at / (2 * GN), g = at / (2 * p.f.N) % p.f.G;
-  if (p.f.seq.state_map) {  // rows without a state have no gradients
-    const int s = p.f.seq.state_map[row / p.f.seq.T];
-    if (s < 0 || s >= p.f.seq.n_state) return;
-  }
-  float sum = 0.f;
+// The sums that are left, in one launch.  The first `bc_groups` workgroups add the channel blocks' dB
+// and dC in their order.  The others add the rows' and segments' shares of dA, d_skip and d_bias, 64
+// columns each (a row is read 256 bytes at a time): each of 16 threads of a column every 16th row,
+// then the 16 sums in order.
+__global__ void __launch_bounds__(1024) ssm_backward_sum_kernel(ScanBackwardParams p, int blocks, unsigned bc_groups) {
+  const ScanSsmParams &f = p.f;
+  if (blockIdx.x < bc_groups) {
+    const long GN = (long)f.G * f.N, total = f.seq.total_tokens * 2 * GN;
+    const long at = (long)blockIdx.x * 1024 + threadIdx.x;
+    if (at >= total) return;
+    const int n = (int)(at % (2 * f.N));
+    const long row = at / (2 * GN), g = at / (2 * f.N) % f.G;
+    if (f.seq.state_map) {  // rows without a state have no gradients
+      const int s = f.seq.state_map[row / f.seq.T];
+      if (s < 0 || s >= f.seq.n_state) return;
+    }
+    float sum = 0.f;
 #pragma unroll 8
-  for (int b = 0; b < blocks; ++b) sum += p.part_bc[b * total + at];
-  const long to = row * GN + g * p.f.N;
-  if (n < p.f.N) store1(p.dB, to + n, p.grad_bf16, sum);
-  else store1(p.dC, to + n - p.f.N, p.grad_bf16, sum);
-}
-
-// out[c] = sum over r of in[r][c]: each of 16 threads adds every 16th row, then the 16 sums in
-// order; 64 columns a workgroup, so that a row is read 256 bytes at a time.
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *in, float *out, long rows, long cols, long stride) {
+    for (int b = 0; b < blocks; ++b) sum += p.part_bc[b * total + at];
+    const long to = row * GN + g * f.N;
+    if (n < f.N) store1(p.dB, to + n, p.grad_bf16, sum);
+    else store1(p.dC, to + n - f.N, p.grad_bf16, sum);
+    return;
+  }
   __shared__ float s[16][64];
   const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
-  const long col = (long)blockIdx.x * 64 + c;
+  const long DN = (long)f.D * f.N, cols = DN + 2L * f.D, rows = (long)f.seq.units * p.nseg;
+  const long col = (long)(blockIdx.x - bc_groups) * 64 + c;
   float a = 0.f;
   if (col < cols) {
 #pragma unroll 8
-    for (long r = k; r < rows; r += 16) a += in[r * stride + col];
+    for (long r = k; r < rows; r += 16) a += p.part[r * cols + col];
   }
   s[k][c] = a;
   __syncthreads();
   if (k == 0 && col < cols) {
     float t = 0.f;
     for (int i = 0; i < 16; ++i) t += s[i][c];
-    out[col] = t;
+    if (col < DN) p.dA[col] = t;
+    else if (col < DN + f.D) { if (p.d_skip) p.d_skip[col - DN] = t; }
+    else if (p.d_bias) p.d_bias[col - DN - f.D] = t;
   }
 }
 
@@ -519,8 +524,9 @@ hipError_t go(const ScanBackwardParams &p, hipStream_t s) {
     else if (rows == Rows::kOverlap) go_rows<BF16, Rows::kOverlap, LN>(p, blocks, s);
   }
   if (rows == Rows::kSingle) go_rows<BF16, Rows::kSingle, LN>(p, blocks, s);
-  const long values = p.f.seq.total_tokens * 2 * p.f.G * p.f.N;
-  hipLaunchKernelGGL(ssm_backward_bc_kernel, dim3((unsigned)((values + 255) / 256)), dim3(256), 0, s, p, nb);
+  const long values = p.f.seq.total_tokens * 2 * p.f.G * p.f.N, cols = (long)p.f.D * (p.f.N + 2);
+  const unsigned bc_groups = (unsigned)((values + 1023) / 1024);
+  hipLaunchKernelGGL(ssm_backward_sum_kernel, dim3(bc_groups + (unsigned)((cols + 63) / 64)), dim3(1024), 0, s, p, nb, bc_groups);
   return hipGetLastError();
 }
 
@@ -535,11 +541,6 @@ hipError_t by_states(const ScanBackwardParams &p, hipStream_t s) {
   }
 }
 
-hipError_t sum_rows(const float *in, float *out, long rows, long cols, long stride, hipStream_t s) {
-  hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, s, in, out, rows, cols, stride);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 int backward_blocks(int D, int N, int G) {
@@ -551,17 +552,8 @@ int backward_segments(int units, int T, int D, int N, int G, int *seg_len) {
   return best_segments((long)units * G * backward_blocks(D, N, G), T, TT, 1.0, 0.3, 30, seg_len);
 }
 
-hipError_t launch_sum_rows(const float *in, float *out, long rows, long cols, hipStream_t s) {
-  return sum_rows(in, out, rows, cols, cols, s);
-}
-
 hipError_t launch_ssm_scan_backward(const ScanBackwardParams &p, bool bf16, hipStream_t s) {
-  hipError_t e = bf16 ? by_states<true>(p, s) : by_states<false>(p, s);
-  const long parts = (long)p.f.seq.units * p.nseg, DN = (long)p.f.D * p.f.N;
-  if (e == hipSuccess) e = sum_rows(p.part_A, p.dA, parts, DN, DN, s);
-  if (e == hipSuccess && p.d_skip) e = sum_rows(p.part_ch, p.d_skip, parts, p.f.D, 2L * p.f.D, s);
-  if (e == hipSuccess && p.d_bias) e = sum_rows(p.part_ch + p.f.D, p.d_bias, parts, p.f.D, 2L * p.f.D, s);
-  return e;
+  return bf16 ? by_states<true>(p, s) : by_states<false>(p, s);
 }
 
 }  // namespace wkv

@@ -82,15 +82,17 @@ class _Call:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         return t.data_ptr(), _row_step(t, name, lead)
 
-    def output(self, y, out_dtype, shape):
+    def output(self, y, out_dtype):
         code, dt = _out_code(y, out_dtype)
         if y is not None:
-            self.flat(y, "y", shape, dt)
-        elif dt is self.dtype and shape == self.ref.shape and self.ref.is_contiguous():
-            y = torch.empty_like(self.ref)
+            self.flat(y, "y", self.ref.shape, dt)
         else:
-            y = torch.empty(shape, dtype=dt, device=self.ref.device)
+            y = self.like(self.ref, dt)
         return y, code
+
+    def like(self, t, dtype):
+        """An empty contiguous tensor of t's shape."""
+        return torch.empty_like(t) if t.dtype is dtype and t.is_contiguous() else torch.empty(t.shape, dtype=dtype, device=t.device)
 
     def empty(self, shape, dtype=torch.float32):
         return torch.empty(shape, dtype=dtype, device=self.ref.device)
@@ -183,7 +185,7 @@ def ssm_conv_forward(x, weight, bias=None, state=None, state_map=None, *, activa
     B, T, D = x.shape
     W, par = _conv_params(call, weight, bias, activation)
     states, state_out = _dense_states(call, state, state_map, state_out, return_state, B, (W - 1, D))
-    y, oc = call.output(y, out_dtype, x.shape)
+    y, oc = call.output(y, out_dtype)
     _launch(call.dev, _lib.wkv_ssm_conv_forward, B, T, D, W, *call.rows(x, "x", x.shape, 2), call.code, *par, y.data_ptr(), oc,
             *states, call.status(dev_status))
     return y, state_out
@@ -206,8 +208,8 @@ def ssm_conv_backward(x, weight, bias, dy, state=None, state_map=None, *, activa
     if grad_dtype not in _CODES:
         raise TypeError(f"unsupported gradient dtype {grad_dtype} (bfloat16 or float32)")
     ds = call.flat(d_state, "d_state", (B, W - 1, D))
-    dx, dw = call.empty(x.shape, grad_dtype), call.empty((D, W))
-    db = call.empty((D,)) if bias is not None else None
+    dx, dw = call.like(x, grad_dtype), call.like(weight, torch.float32)
+    db = call.like(bias, torch.float32) if bias is not None else None
     d_first = call.empty((B, W - 1, D)) if return_d_state else None
     need = _lib.wkv_ssm_conv_backward_workspace(B, T, D, W)
     ws = call.empty((need // 4,))
@@ -228,7 +230,7 @@ def ssm_conv_forward_varlen(lengths, x, weight, bias, state, *, max_len, state_o
     total, D = x.shape
     W, par = _conv_params(call, weight, bias, activation)
     S, ln, states = _slot_states(call, lengths, state, state_map, state_out, (W - 1, D))
-    y, oc = call.output(y, out_dtype, x.shape)
+    y, oc = call.output(y, out_dtype)
     _launch(call.dev, _lib.wkv_ssm_conv_forward_varlen, S, D, W, ln, int(max_len), total, *call.rows(x, "x", x.shape, 1), call.code,
             *par, y.data_ptr(), oc, *states, call.status(dev_status))
     return y
@@ -272,7 +274,7 @@ def ssm_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, s
     rows, T, _ = x.shape
     width, N, G, args = _scan_args(call, x, dt, A, B, C, D, z, dt_bias, dt_softplus)
     states, state_out = _dense_states(call, state, state_map, state_out, return_state, rows, (width, N))
-    y, oc = call.output(y, out_dtype, x.shape)
+    y, oc = call.output(y, out_dtype)
     ws, ws_bytes = _workspace(call, rows, T, rows * T, width, N, G)
     _launch(call.dev, _lib.wkv_ssm_scan_forward, rows, T, width, N, G, *args, y.data_ptr(), oc, *states, _ptr(ws), ws_bytes,
             call.status(dev_status))
@@ -294,7 +296,7 @@ def ssm_scan_forward_train(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=N
     rows, T, _ = x.shape
     width, N, G, args = _scan_args(call, x, dt, A, B, C, D, z, dt_bias, dt_softplus)
     states, state_out = _dense_states(call, state, state_map, state_out, return_state, rows, (width, N))
-    y, oc = call.output(y, out_dtype, x.shape)
+    y, oc = call.output(y, out_dtype)
     saved = (rows, _chunks(T), width, N)
     if chunk_states is None:
         chunk_states = call.empty(saved)
@@ -326,12 +328,12 @@ def ssm_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, state=No
     dya = call.rows(dy, "dy", x.shape, 2, any_dtype=True)
     chunks = call.flat(chunk_states, "chunk_states", (rows, _chunks(T), width, N)) or None
     ds = call.flat(d_state, "d_state", (rows, width, N))
-    dx, ddt = call.empty(x.shape, grad_dtype), call.empty(x.shape, grad_dtype)
-    dB, dC = call.empty(B.shape, grad_dtype), call.empty(C.shape, grad_dtype)
-    dz = call.empty(x.shape, grad_dtype) if z is not None else None
-    dA = call.empty((width, N))
-    dD = call.empty((width,)) if D is not None else None
-    db = call.empty((width,)) if dt_bias is not None else None
+    dx, ddt = call.like(x, grad_dtype), call.like(dt, grad_dtype)
+    dB, dC = call.like(B, grad_dtype), call.like(C, grad_dtype)
+    dz = call.like(z, grad_dtype) if z is not None else None
+    dA = call.like(A, torch.float32)
+    dD = call.like(D, torch.float32) if D is not None else None
+    db = call.like(dt_bias, torch.float32) if dt_bias is not None else None
     d_first = call.empty((rows, width, N)) if return_d_state else None
     need = _lib.wkv_ssm_scan_backward_workspace(rows, T, width, N, G, int(chunks is not None or _chunks(T) == 0))
     ws = call.empty((need // 4,))
@@ -352,7 +354,7 @@ def ssm_scan_forward_varlen(lengths, x, dt, A, B, C, state, *, max_len, D=None, 
     total = x.shape[0]
     width, N, G, args = _scan_args(call, x, dt, A, B, C, D, z, dt_bias, dt_softplus)
     S, ln, states = _slot_states(call, lengths, state, state_map, state_out, (width, N))
-    y, oc = call.output(y, out_dtype, x.shape)
+    y, oc = call.output(y, out_dtype)
     ws, ws_bytes = _workspace(call, S, int(max_len), total, width, N, G)
     _launch(call.dev, _lib.wkv_ssm_scan_forward_varlen, S, width, N, G, ln, int(max_len), total, *args, y.data_ptr(), oc,
             *states, _ptr(ws), ws_bytes, call.status(dev_status))
