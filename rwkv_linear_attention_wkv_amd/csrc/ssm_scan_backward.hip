@@ -141,12 +141,18 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
         for (int i = 0; i < 4; ++i) g0[i] = fmaf(__builtin_amdgcn_exp2f(sum * A[i]), g0[i], from[i]);
       }
     }
-    // the state at the start of the tile at t0
-    const auto state_at = [&](int t0, float (&h)[4]) {
+    // The state at the start of the tile at t0, without a branch: where paths join, the compiler would
+    // copy what is loaded and wait for it at once, here for a whole load a tile (498 us instead of 445 at
+    // [8, 2048, 2048], N = 16).
+    uint32_t value[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = 0.f;
-      if (t0) load_state4(f.chunk_states + (((long)unit * f.n_chunks + t0 / TT - 1) * D + d) * N, q, N, whole, h);
-      else if (f.seq.state_in) load_state4(f.seq.state_in + ((long)sq.row_in * D + d) * N, q, N, whole, h);
+    for (int i = 0; i < 4; ++i) value[i] = (ch * N + 4 * q + i) * 4 + (live && 4 * q + i < N ? 0u : kOutside);
+    const auto state_at = [&](int t0, float (&h)[4]) {
+      const float *from = t0 ? f.chunk_states : f.seq.state_in;
+      const long row = t0 ? (long)unit * f.n_chunks + t0 / TT - 1 : sq.row_in;
+      const auto w = window<4>(from, slot, from ? row : 0, from ? 1 : 0, d0 * N, c_live * N);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w, value[i], 0, 0));
     };
     float h0[4], dA[4] = {0.f, 0.f, 0.f, 0.f}, total = 0.f;
     f32x4 G = {g0[0], g0[1], g0[2], g0[3]};
@@ -180,8 +186,8 @@ __global__ void __launch_bounds__(512, 2) ssm_scan_backward_kernel(ScanBackwardP
           sum[u % LN] = fmaf(C.w, h[u][3], fmaf(C.z, h[u][2], fmaf(C.y, h[u][1], C.x * h[u][0])));
           if (u % LN == LN - 1) s_out[buf][0][u - (LN - 1) + q][ch] = spread4<LN>(sum, q);
         }
-        float next[4] = {0.f, 0.f, 0.f, 0.f};  // the state of the tile that comes next: on its way during this one
-        if (k + 1 < tiles) state_at(t0 - TT, next);
+        float next[4];  // the state of the tile that comes next: on its way during this one
+        state_at(max(t0 - TT, 0), next);  // (after the last tile, not used)
         float gb[LN], ga[LN];
 #pragma unroll
         for (int u = TT - 1; u >= 0; --u) {
