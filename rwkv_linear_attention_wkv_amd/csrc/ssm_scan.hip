@@ -12,68 +12,76 @@ namespace {
 
 // Few tokens (single-token steps): LN adjacent lanes share a channel, four states each, and walk the
 // tokens one by one.  Bound by the states' way in and out, one coalesced load and store of 16 bytes a
-// lane; a token's loads leave together, the first token's with the state's.
-template <bool BF16>
+// lane, and by the latencies in a row: so every load goes through a window, which answers what is not
+// there with zeros, and none waits behind another's branch.  A token's values and the state leave
+// together; the state, the longest way, is asked for last and waited for last.
+template <bool BF16, bool WHOLE>
 struct ShortToken {
-  float x, dt, z;
-  float B[4], C[4];
-  __device__ __forceinline__ void load(const ScanSsmParams &p, long row, long d, long bc, int n) {
-    x = load1<BF16>(p.x.base, row * p.x.stride + d);
-    dt = load1<BF16>(p.dt.base, row * p.dt.stride + d);
-    z = p.z.base ? load1<BF16>(p.z.base, row * p.z.stride + d) : 0.f;
-    if ((p.N & 3) == 0) {  // every lane's four values are a whole load
-      const long at = bc + (n < p.N ? n : 0);
-      loadv<BF16>(p.Bm.base, row * p.Bm.stride + at, B);
-      loadv<BF16>(p.Cm.base, row * p.Cm.stride + at, C);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long at = bc + (n + i < p.N ? n + i : 0);
-        B[i] = load1<BF16>(p.Bm.base, row * p.Bm.stride + at);
-        C[i] = load1<BF16>(p.Cm.base, row * p.Cm.stride + at);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i >= p.N) B[i] = C[i] = 0.f;
+  static constexpr int EL = BF16 ? 2 : 4;
+  RawRow<BF16, false, 1> x, dt, z;
+  RawRow<BF16, WHOLE, 4> B, C;
+  // of the token `row`, if `rows` is 1; col: of the lane's channel and states, in elements
+  __device__ __forceinline__ void load(const ScanSsmParams &p, long row, int rows, long d0, int c_live, long bc, const uint32_t (&c_col)[1],
+                                       const uint32_t (&n_col)[WHOLE ? 1 : 4]) {
+    x.load(window<EL>(p.x.base, p.x.stride, row, rows, d0, c_live), 0, c_col);
+    dt.load(window<EL>(p.dt.base, p.dt.stride, row, rows, d0, c_live), 0, c_col);
+    z.load(window<EL>(p.z.base, p.z.stride, row, p.z.base ? rows : 0, d0, c_live), 0, c_col);
+    B.load(window<EL>(p.Bm.base, p.Bm.stride, row, rows, bc, p.N), 0, n_col);
+    C.load(window<EL>(p.Cm.base, p.Cm.stride, row, rows, bc, p.N), 0, n_col);
   }
 };
 
-template <bool BF16, int LN>
+// WHOLE: N divides by 4, so that a lane's four states are there or not as one.
+template <bool BF16, int LN, bool WHOLE>
 __global__ void __launch_bounds__(256) ssm_scan_short_kernel(ScanSsmParams p) {
-  constexpr int CH = 256 / LN;  // channels of a workgroup
-  const int lane = threadIdx.x & 63, q = threadIdx.x % LN;
+  constexpr int CH = 256 / LN, EL = BF16 ? 2 : 4, NC = WHOLE ? 1 : 4;  // CH: channels of a workgroup
+  const int lane = threadIdx.x & 63, q = threadIdx.x % LN, ch = threadIdx.x / LN, N = p.N;
   const int per_group = p.D / p.G, blocks = (per_group + CH - 1) / CH;
-  const int g = blockIdx.x / blocks, in_group = (blockIdx.x % blocks) * CH + threadIdx.x / LN;
-  const bool live = in_group < per_group;
-  const long d = (long)g * per_group + (live ? in_group : 0);
-  const int N = p.N;
-  const bool whole = (N & 3) == 0 && 4 * q < N;
-  float A[4], h[4] = {0.f, 0.f, 0.f, 0.f};
-  load_decay4(p.A + d * N, q, N, whole, A);
-  const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
+  const int g = blockIdx.x / blocks, c_base = (blockIdx.x % blocks) * CH, c_live = min(CH, per_group - c_base);
+  const bool live = ch < c_live;
+  const long d0 = (long)g * per_group + c_base;
+  uint32_t n_col[NC], s_col[NC];  // of B and C, and of fp32 rows [D, N] from d0 on
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const uint32_t out = 4 * q + i < N ? 0u : kOutside;
+    n_col[i] = (4 * q + i) * EL + out;
+    s_col[i] = (ch * N + 4 * q + i) * 4 + (live ? out : kOutside);
+  }
+  const uint32_t c_col[1] = {ch * EL + (live ? 0u : kOutside)}, f_col[1] = {ch * 4 + (live ? 0u : kOutside)};
+  const long slot = (long)p.D * N;
+  RawRow<false, false, 1> raw_bias, raw_skip;
+  RawRow<false, WHOLE, 4> raw_A, raw_h;
+  raw_A.load(window<4>(p.A, slot, 0, 1, d0 * N, c_live * N), 0, s_col);
+  raw_bias.load(window<4>(p.dt_bias, p.D, 0, p.dt_bias ? 1 : 0, d0, c_live), 0, f_col);
+  raw_skip.load(window<4>(p.skip, p.D, 0, p.skip ? 1 : 0, d0, c_live), 0, f_col);
   const Sequence sq = find_sequence(p.seq, blockIdx.y, lane);
   if (!sq.ok) return;
-  if (p.seq.state_in) load_state4(p.seq.state_in + ((long)sq.row_in * p.D + d) * N, q, N, whole, h);
-  ShortToken<BF16> now, next;
-  if (sq.len > 0) now.load(p, sq.off, d, (long)g * N, 4 * q);
+  ShortToken<BF16, WHOLE> now, next;
+  now.load(p, sq.off, sq.len > 0, d0, c_live, (long)g * N, c_col, n_col);
+  raw_h.load(window<4>(p.seq.state_in, slot, sq.row_in, p.seq.state_in ? 1 : 0, d0 * N, c_live * N), 0, s_col);
+  float A[4], h[4];
+  const float bias = raw_bias.get(0), skip = raw_skip.get(0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = decay_rate(raw_A.get(i));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = raw_h.get(i);
   for (int t = 0; t < sq.len; ++t) {
     const long r = sq.off + t;
-    if (t + 1 < sq.len) next.load(p, r + 1, d, (long)g * N, 4 * q);
-    const float raw = now.dt + bias, delta = p.softplus ? softplus_f(raw) : raw, dx = delta * now.x;
+    next.load(p, r + 1, t + 1 < sq.len, d0, c_live, (long)g * N, c_col, n_col);
+    const float x = now.x.get(0), raw = now.dt.get(0) + bias, delta = p.softplus ? softplus_f(raw) : raw, dx = delta * x;
     float part = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      h[i] = fmaf(__builtin_amdgcn_exp2f(delta * A[i]), h[i], dx * now.B[i]);
-      part = fmaf(now.C[i], h[i], part);
+      h[i] = fmaf(__builtin_amdgcn_exp2f(delta * A[i]), h[i], dx * now.B.get(i));
+      part = fmaf(now.C.get(i), h[i], part);
     }
-    float y = fmaf(skip, now.x, sum_all<LN>(part));
-    if (p.z.base) y *= now.z * sigmoid_f(now.z);
-    if (live && q == 0) store1(p.y, r * p.D + d, p.y_bf16, y);
+    float y = fmaf(skip, x, sum_all<LN>(part));
+    if (p.z.base) y *= now.z.get(0) * sigmoid_f(now.z.get(0));
+    if (live && q == 0) store1(p.y, r * p.D + d0 + ch, p.y_bf16, y);
     now = next;
   }
   if (live && p.seq.state_out && !(sq.len == 0 && p.seq.state_out == p.seq.state_in))
-    store_state4(p.seq.state_out + ((long)sq.row_out * p.D + d) * N, q, N, whole, h);
+    store_state4(p.seq.state_out + sq.row_out * slot + (d0 + ch) * N, q, N, WHOLE && 4 * q < N, h);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -420,7 +428,8 @@ hipError_t go(const ScanSsmParams &p, hipStream_t s) {
   constexpr int CH = 256 / LN, VW = Tile<LN>::VW;
   const int per_group = p.D / p.G, blocks = p.G * ((per_group + CH - 1) / CH);
   if (p.seq.T <= kScanShort && p.y) {
-    hipLaunchKernelGGL((ssm_scan_short_kernel<BF16, LN>), dim3(blocks, p.seq.units), dim3(256), 0, s, p);
+    if (p.N % 4 == 0) hipLaunchKernelGGL((ssm_scan_short_kernel<BF16, LN, true>), dim3(blocks, p.seq.units), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((ssm_scan_short_kernel<BF16, LN, false>), dim3(blocks, p.seq.units), dim3(256), 0, s, p);
     return hipGetLastError();
   }
   const Rows rows = rows_of<CH, VW>(per_group);

@@ -16,16 +16,18 @@ __device__ __forceinline__ void load_state4(const float *row, int q, int N, bool
   }
 }
 
-// Four values of A, scaled for the base-2 exponential, and finite, so that a step of zero (a token past
+// A value of A, scaled for the base-2 exponential, and finite, so that a step of zero (a token past
 // a sequence's end, too) is a decay of one also where A or its scaled value is an infinity.
-__device__ __forceinline__ void load_decay4(const float *row, int q, int N, bool whole, float (&A)[4]) {
+__device__ __forceinline__ float decay_rate(float A) {
   constexpr float kMost = 3.4028234663852886e38f;
+  A *= kLog2e;
+  return A < -kMost ? -kMost : A > kMost ? kMost : A;  // NaN stays
+}
+
+__device__ __forceinline__ void load_decay4(const float *row, int q, int N, bool whole, float (&A)[4]) {
   load_state4(row, q, N, whole, A);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    A[i] *= kLog2e;
-    A[i] = A[i] < -kMost ? -kMost : A[i] > kMost ? kMost : A[i];  // NaN stays
-  }
+  for (int i = 0; i < 4; ++i) A[i] = decay_rate(A[i]);
 }
 
 __device__ __forceinline__ void store_state4(float *row, int q, int N, bool whole, const float (&h)[4]) {
