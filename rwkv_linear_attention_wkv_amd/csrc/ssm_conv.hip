@@ -46,9 +46,12 @@ __device__ __forceinline__ void conv_walk(const ConvParams &p, int seg, long c) 
   const auto wy = window<YEL>(p.y, p.D, q.off + t0, t1 - t0, 0, p.D);
   const uint32_t col[1] = {(uint32_t)c * EL}, ycol[1] = {(uint32_t)c * YEL};
   const uint32_t step = (uint32_t)p.x.stride * EL, ystep = (uint32_t)p.D * YEL;
-  Raw x[U];
+  Raw x[2][U];  // rounds in turn, so that none is copied (a copy waits for its loads)
+  const auto request = [&](Raw (&to)[U], int t) {  // rows past the segment read 0, and their results are not written
 #pragma unroll
-  for (int u = 0; u < U; ++u) x[u].load(wx, u * step, col);
+    for (int u = 0; u < U; ++u) to[u].load(wx, (t + u) * step, col);
+  };
+  request(x[0], 0);
 
   if (seg == 0) {
 #pragma unroll
@@ -81,16 +84,18 @@ __device__ __forceinline__ void conv_walk(const ConvParams &p, int seg, long c) 
     for (int i = 0; i < W - 1; ++i) loadv<BF16>(p.x.base, (q.off + t0 - (W - 1) + i) * p.x.stride + c, prev[i]);
   }
 
-  for (int t = 0; t < t1 - t0; t += U) {
-    Raw next[U];  // rows past the segment read 0, and their results are not written
+  const auto arrive = [&](Raw (&now)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) next[u].load(wx, (t + U + u) * step, col);
+    for (int u = 0; u < U; ++u) now[u].arrive();
+  };
+  const auto round = [&](Raw (&now)[U], int t) {
+    arrive(now);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float y[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float xe = x[u].get(e);
+        const float xe = now[u].get(e);
         float a = bias[e];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], prev[j][e], a);
@@ -102,8 +107,16 @@ __device__ __forceinline__ void conv_walk(const ConvParams &p, int seg, long c) 
       }
       store_row<YBF16, VEC, V>(wy, (t + u) * ystep, ycol, y);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) x[u] = next[u];
+  };
+  for (int t = 0; t < t1 - t0; t += 2 * U) {
+    request(x[1], t + U);
+    round(x[0], t);
+    if (t + U >= t1 - t0) {
+      arrive(x[1]);  // (else the compiler waits at the head of the loop, for every round)
+      break;
+    }
+    request(x[0], t + 2 * U);
+    round(x[1], t + U);
   }
 }
 
@@ -166,76 +179,90 @@ __device__ __forceinline__ void conv_walk_back(const ConvParams &p, int seg, lon
     const auto wd = window<DEL>(p.dy.base, p.dy.stride, q.off + t0, rows, 0, p.D);
     const uint32_t col[1] = {(uint32_t)c * EL}, dcol[1] = {(uint32_t)c * DEL};
     const uint32_t step = (uint32_t)p.x.stride * EL, dstep = (uint32_t)p.dy.stride * DEL;
-    RawRow<BF16, VEC, V> rx[U];
-    RawRow<DYBF16, VEC, V> ry[U];
+    // Only the rows of this segment: the walk's first and last steps form others, which are not written.
+    const auto wg = p.y_bf16 ? window<2>(p.y, p.D, q.off + t0, t1 - t0, 0, p.D) : window<4>(p.y, p.D, q.off + t0, t1 - t0, 0, p.D);
+    const uint32_t gcol[1] = {(uint32_t)c * (p.y_bf16 ? 2 : 4)}, gstep = (uint32_t)p.D * (p.y_bf16 ? 2 : 4);
+    struct Round {  // two in turn, so that none is copied (a copy waits for its loads)
+      RawRow<BF16, VEC, V> x[U];
+      RawRow<DYBF16, VEC, V> dy[U];
+      __device__ __forceinline__ void arrive() {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rx[u].load(wx, u * step, col);
-      ry[u].load(wd, u * dstep, dcol);
-    }
+        for (int u = 0; u < U; ++u) { x[u].arrive(); dy[u].arrive(); }
+      }
+    } rounds[2];
+    const auto request = [&](Round &to, int t) {  // rows past the sequence or the walk read 0
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        to.x[u].load(wx, (t + u) * step, col);
+        to.dy[u].load(wd, (t + u) * dstep, dcol);
+      }
+    };
+    request(rounds[0], 0);
     load_taps(p, c, w, bias);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < W; ++i)  // one place early: the walk shifts before it uses them
 #pragma unroll
       for (int e = 0; e < V; ++e) x[i][e] = d[i][e] = 0.f;
-      const int t = t0 - W + i;  // one place early: the loop shifts before it uses them
-      if (i > 0) {
-        if (t >= 0) loadv<BF16>(p.x.base, (q.off + t) * p.x.stride + c, x[i]);
-        else if (p.seq.state_in) loadv<false>(p.seq.state_in, ((long)q.row_in * (W - 1) + t + W - 1) * p.D + c, x[i]);
-      }
+    if (seg) {
+#pragma unroll
+      for (int i = 1; i < W; ++i) loadv<BF16>(p.x.base, (q.off + t0 - W + i) * p.x.stride + c, x[i]);
+    } else if (p.seq.state_in) {
+#pragma unroll
+      for (int i = 1; i < W; ++i) loadv<false>(p.seq.state_in, ((long)q.row_in * (W - 1) + i - 1) * p.D + c, x[i]);
     }
-    for (int tb = t0; tb < end; tb += U) {
-      RawRow<BF16, VEC, V> nx[U];  // rows past the sequence or the walk read 0
-      RawRow<DYBF16, VEC, V> ny[U];
+    const auto walk = [&](Round &now, int from) {
+      now.arrive();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        nx[u].load(wx, (tb - t0 + U + u) * step, col);
-        ny[u].load(wd, (tb - t0 + U + u) * dstep, dcol);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u;
-        const bool own = t < t1;  // its share of the taps' gradients is this segment's
+        const int t = t0 + from + u;
         float g[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
 #pragma unroll
           for (int i = 0; i < W - 1; ++i) { x[i][e] = x[i + 1][e]; d[i][e] = d[i + 1][e]; }
-          x[W - 1][e] = rx[u].get(e);
-          float grad = ry[u].get(e);
-          if (p.silu) {
-            float a = bias[e];
+          x[W - 1][e] = now.x[u].get(e);
+          const float grad = now.dy[u].get(e);
+          float a = bias[e];
 #pragma unroll
-            for (int j = 0; j < W; ++j) a = fmaf(w[j][e], x[j][e], a);
-            const float sg = sigmoid_f(a);
-            grad *= sg * fmaf(a, 1.f - sg, 1.f);
-          }
-          grad = t < q.len ? grad : 0.f;
-          d[W - 1][e] = grad;
-          const float mine = own ? grad : 0.f;
-#pragma unroll
-          for (int j = 0; j < W; ++j) dw[j][e] = fmaf(mine, own ? x[j][e] : 0.f, dw[j][e]);
-          dw[W][e] += mine;
+          for (int j = 0; j < W; ++j) a = fmaf(w[j][e], x[j][e], a);
+          const float sg = sigmoid_f(a), through = p.silu ? grad * (sg * fmaf(a, 1.f - sg, 1.f)) : grad;
+          d[W - 1][e] = t < q.len ? through : 0.f;
           float v = 0.f;
 #pragma unroll
           for (int i = 0; i < W; ++i) v = fmaf(w[W - 1 - i][e], d[i][e], v);
           g[e] = v;
         }
-        const int s = t - (W - 1), last = s - (q.len - (W - 1));  // last >= 0: the input is a row of the final state
-        if (t < end && (s >= t0 || (seg == 0 && p.d_state_in))) {
-          if (last >= 0 && p.d_state_out) {
-            float more[V];
-            loadv<false>(p.d_state_out, ((long)blockIdx.y * (W - 1) + last) * p.D + c, more);
+        if (t < t1) {  // the taps' gradients of other tokens are another segment's
 #pragma unroll
-            for (int e = 0; e < V; ++e) g[e] += more[e];
+          for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j][e] = fmaf(d[W - 1][e], x[j][e], dw[j][e]);
+            dw[W][e] += d[W - 1][e];
           }
-          if (s < 0) storev<false>(p.d_state_in, ((long)blockIdx.y * (W - 1) + s + W - 1) * p.D + c, g);
-          else if (p.y_bf16) storev<true>(p.y, (q.off + s) * p.D + c, g);
-          else storev<false>(p.y, (q.off + s) * p.D + c, g);
         }
-      }
+        const int s = t - (W - 1), last = s - (q.len - (W - 1));  // last >= 0: the input is a row of the final state
+        if (last >= 0 && t < end && p.d_state_out) {
+          float more[V];
+          loadv<false>(p.d_state_out, ((long)blockIdx.y * (W - 1) + last) * p.D + c, more);
 #pragma unroll
-      for (int u = 0; u < U; ++u) { rx[u] = nx[u]; ry[u] = ny[u]; }
+          for (int e = 0; e < V; ++e) g[e] += more[e];
+        }
+        const uint32_t at = (uint32_t)(s - t0) * gstep;  // before the window: beyond its end
+        if (p.y_bf16) store_row<true, VEC, V>(wg, at, gcol, g);
+        else store_row<false, VEC, V>(wg, at, gcol, g);
+        if (s < 0 && seg == 0 && t < end && p.d_state_in)
+          storev<false>(p.d_state_in, ((long)blockIdx.y * (W - 1) + s + W - 1) * p.D + c, g);
+      }
+    };
+    for (int t = 0; t < end - t0; t += 2 * U) {
+      request(rounds[1], t + U);
+      walk(rounds[0], t);
+      if (t + U >= end - t0) {
+        rounds[1].arrive();  // (else the compiler waits at the head of the loop, for every round)
+        break;
+      }
+      request(rounds[0], t + 2 * U);
+      walk(rounds[1], t + U);
     }
   }
   const long row = (long)blockIdx.y * p.nseg + seg;
