@@ -52,7 +52,7 @@ struct ConvParams {
 
 hipError_t launch_ssm_conv(const ConvParams &p, bool bf16, hipStream_t s);
 hipError_t launch_ssm_conv_backward(const ConvParams &p, bool bf16, hipStream_t s);
-int conv_segments(int units, int T, int D, bool backward, int *seg_len);
+int conv_segments(int T, long total, int D, bool bf16, bool backward, int *seg_len);
 
 struct ScanSsmParams {
   SeqParams seq;

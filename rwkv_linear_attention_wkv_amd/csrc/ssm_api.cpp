@@ -109,7 +109,7 @@ wkv_status conv(const char *fn, const wkv::SeqParams &seq, int D, int W, const v
   p.weight = weight; p.bias = bias;
   p.silu = act == WKV_ACT_SILU;
   p.y = y; p.y_bf16 = out_dtype == WKV_BF16;
-  p.nseg = wkv::conv_segments(seq.units, seq.T, D, false, &p.seg_len);
+  p.nseg = wkv::conv_segments(seq.T, seq.total_tokens, D, in_dtype == WKV_BF16, false, &p.seg_len);
   return launched(wkv::launch_ssm_conv(p, in_dtype == WKV_BF16, static_cast<hipStream_t>(stream)), fn);
 }
 
@@ -254,7 +254,7 @@ wkv_status wkv_ssm_conv_forward_varlen(int num_slots, int D, int W, const int32_
 size_t wkv_ssm_conv_backward_workspace(int B, int T, int D, int W) {
   if (B < 1 || T < 1 || D < 1 || W < 2 || W > 4) return 0;
   int len;
-  return sizeof(float) * (size_t)B * wkv::conv_segments(B, T, D, true, &len) * (W + 1) * D;
+  return sizeof(float) * (size_t)B * wkv::conv_segments(T, (long)B * T, D, true, true, &len) * (W + 1) * D;
 }
 
 wkv_status wkv_ssm_conv_backward(int B, int T, int D, int W, const void *x, int64_t x_stride, wkv_dtype in_dtype,
@@ -288,7 +288,7 @@ wkv_status wkv_ssm_conv_backward(int B, int T, int D, int W, const void *x, int6
   p.d_state_out = d_state_out; p.d_state_in = d_state_in;
   p.partial = static_cast<float *>(workspace);
   p.d_weight = d_weight; p.d_bias = d_bias;
-  p.nseg = wkv::conv_segments(B, T, D, true, &p.seg_len);
+  p.nseg = wkv::conv_segments(T, (long)B * T, D, in_dtype == WKV_BF16, true, &p.seg_len);
   return launched(wkv::launch_ssm_conv_backward(p, in_dtype == WKV_BF16, static_cast<hipStream_t>(stream)), fn);
 }
 
