@@ -5,9 +5,11 @@
 //
 // Bound by memory: one read of x and one write of y.  A lane owns V adjacent channels (one load of
 // up to 16 bytes) and walks a segment of the sequence with the last W - 1 inputs in registers, so
-// that an input is read once but for the W - 1 before each segment; loads run U tokens ahead.  The
-// first segment also owns the state: it reads it, and writes the new one, so that a call may update
-// it in place.
+// that an input is read once but for the W - 1 before each segment; loads run U tokens ahead, into two
+// sets of registers in turn.  The first segment also owns the state: it reads it, and writes the new
+// one, so that a call may update it in place.  [8, 4096, 4096] bf16, W = 4: 108 us, 4.97 TB/s, what a
+// plain copy of that size reaches (116 us with one set that each round was copied into); a step of 64
+// slots, D = 2048: 6.7 us, of which an empty launch is 2.9 and the bytes 0.7.
 #include "ssm_tile.hpp"
 
 namespace wkv {
@@ -159,7 +161,8 @@ hipError_t by_width(const ConvParams &p, hipStream_t s) {
 //   state before the first token is such an input too);  dweight[j] = sum_t d_t x_(t-W+1+j), dbias = sum_t d_t
 // One read of x and dy, one write of dx: a lane walks its segment once with the last W - 1 inputs and d
 // in registers, W - 1 tokens past its end.  The sums over tokens leave one row per segment, which a
-// second kernel adds in order.
+// second kernel adds in order.  [4, 2047, 2048] bf16, W = 4: 25.8 us (3.9 TB/s; some 45 vector
+// instructions a value stand beside its 6 bytes) and 4.0 us for the sums.
 template <bool BF16, bool DYBF16, int W, int V>
 __device__ __forceinline__ void conv_walk_back(const ConvParams &p, int seg, long c) {
   const Sequence q = find_sequence(p.seq, blockIdx.y, threadIdx.x & 63);

@@ -5,7 +5,9 @@
 // scale 0; a group that holds an infinity or NaN has scale NaN and reads back as NaN throughout.
 //
 // Bound by memory (4 bytes in, 1 + 1/16 out, or the reverse): 16 lanes share a group, four values
-// each, so a wave reads 1 KiB in one load; the group's largest magnitude is four DPP steps.
+// each, so a wave reads 1 KiB in one load; the group's largest magnitude is four DPP steps.  A set of
+// lanes takes four groups at once, for loads enough in flight.  Writing 64 rows of 131072 values: 8.7 us,
+// 4.9 TB/s (13.9 us with a group at a time and divisions).
 #include "ssm_device.hpp"
 
 namespace wkv {
