@@ -326,6 +326,7 @@ hipError_t backward_by_width(const ConvParams &p, hipStream_t s) {
 int conv_segments(int T, long total, int D, bool bf16, bool backward, int *seg_len) {
   const int V = bf16 && !backward ? 8 : 4;
   const long per_token = (D / V + 63) / 64;  // total counts the tokens that slots of unlike lengths have
+  if (T > total) T = (int)total;  // no slot has more tokens than the call, whatever the host's bound
   int len = 64;
   while (len > 16 && per_token * total < (backward ? 1920L : 960L) * len) len /= 2;
   *seg_len = len;

@@ -495,6 +495,7 @@ int best_segments(long groups, int T, int step, double shared, double carry, int
 // total / T stands for the full-length rows of a call whose slots differ.
 int scan_segments(int units, int T, long total, int D, int N, int G, int *seg_len) {
   const int CH = 256 / lanes_of(N);
+  if (T > total) T = (int)total;  // no slot has more tokens than the call, whatever the host's bound
   const long full = T > 0 && total / T + 1 < units ? total / T + 1 : units;
   return best_segments(full * G * ((D / G + CH - 1) / CH), T, 32, 0.88, 0.7, 64, seg_len);
 }

@@ -88,6 +88,8 @@ def test_scan_workspace(lib):
         assert lib.wkv_ssm_scan_workspace(*bad) == 0
     assert scan(lib, B=1, T=4096, ws=P, wb=need - 1) == E and b"workspace" in lib.wkv_last_error()
     assert scan(lib, B=1, T=4096, ws=0x10008, wb=need) == E
+    # a bound on the lengths above the tokens of the call counts as the tokens
+    assert lib.wkv_ssm_scan_workspace(4, 1 << 30, 5000, 256, 16, 1) == lib.wkv_ssm_scan_workspace(4, 5000, 5000, 256, 16, 1) > 0
 
 
 def store(fn, data=P, scale=P, n=4, fmt=0, st=P, ns=4, row=64, sr=None, tr=None, count=4, ds=None):

@@ -437,6 +437,21 @@ def test_scan_varlen(lengths, dtype, D, N, G):
     assert (out.cpu()[keep] == 5).all() and torch.equal(out.cpu()[~keep], st.cpu()[~keep])
 
 
+def test_varlen_bound_far_above_the_tokens():
+    """The host's bound may be anything: work is launched for the tokens there are."""
+    lengths, D, N = [5, 30, 0, 1], 40, 16
+    c = scan_case(0, 0, D, N, 0, F32, seed=77, lead=(sum(lengths),), n_state=len(lengths))
+    ln = gpu(torch.tensor(lengths, dtype=torch.int32))
+    args, weight = [gpu(c[k]) for k in ("x", "dt", "A", "B", "C")], gpu(draw(78, D, 4))
+    got = []
+    for bound in (max(lengths), (1 << 30)):
+        st, tail = gpu(c["state"]), gpu(draw(79, len(lengths), 3, D))
+        got.append((wkv.ssm_scan_forward_varlen(ln, *args, st, max_len=bound),
+                    wkv.ssm_conv_forward_varlen(ln, args[0], weight, None, tail, max_len=bound), st, tail))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------------------- data errors, slots
 
 def slot_call(kind, lengths, state_map, n_state, total, max_len):
