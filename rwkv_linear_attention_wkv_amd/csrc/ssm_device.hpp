@@ -201,7 +201,7 @@ __device__ __forceinline__ float softplus_e(float v, float e) {
   r = fmaf(r, e, 0.3331909775733948f);
   r = fmaf(r, e, -0.4999949336051941f);
   r = fmaf(r, e, 0.9999999403953552f);
-  return fmaf(e, r, fmaxf(v, 0.f));
+  return fmaf(e, r, __int_as_float(max(__float_as_int(v), 0)));  // max(v, 0) in one instruction; a NaN comes with e
 }
 
 __device__ __forceinline__ float softplus_f(float v) {

@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(256) ssm_scan_short_kernel(ScanSsmParams p) {
 //     values and four delta x, so that a state costs a lane a multiply, an exponential and two
 //     multiply-adds.  (fp32 throughout; y on the matrix unit as well was slower: 367 us, not 314.)
 //     The partial sums over n are spread over the LN lanes, LN tokens at a time.
-// [8, 4096, 2048], N = 16, bf16: 280 us.  An exponential and three multiply-adds of a state take a SIMD 23
-// cycles a wave (169 us in all), the staging waves' 50 instructions of a token and channel 105 us
-// more; the vector ALUs are busy for 0.75 of the time, the bytes would take 109 us.  Without the two
+// [8, 4096, 2048], N = 16, bf16: 280 us.  A scan wave's token is 20 vector instructions, four of them
+// exponentials of two turns (179 us in all at 2.23 GHz), a staging wave's token and channel 33 turns (61 us
+// more); the vector ALUs are busy for 0.75 of the time, the bytes would take 109 us.  Without the two
 // roles, one set of waves doing both in turn: 421 us.
 //
 // Few rows: the sequence is cut into nseg segments.  The carry pass runs all but the last from a
