@@ -222,6 +222,25 @@ WKV_API wkv_status wkv_state_store_read(const void *data, const float *scale, in
                         const int32_t *store_rows, const int32_t *state_rows, int count,
                         int32_t *dev_status, void *stream);
 
+/*
+ * One of the calls above with its arguments in order as `count` words: integers,
+ * and pointers as their addresses (host memory, read before the call returns).
+ * For callers to whom passing each argument by itself is dear, such as
+ * interpreters.  WKV_ERR_INVALID_ARG for an unknown op, another count, or an
+ * integer that its parameter cannot hold.
+ */
+typedef int32_t wkv_ssm_op;
+#define WKV_OP_CONV_FORWARD 0
+#define WKV_OP_CONV_FORWARD_VARLEN 1
+#define WKV_OP_CONV_BACKWARD 2
+#define WKV_OP_SCAN_FORWARD 3
+#define WKV_OP_SCAN_FORWARD_TRAIN 4
+#define WKV_OP_SCAN_FORWARD_VARLEN 5
+#define WKV_OP_SCAN_BACKWARD 6
+#define WKV_OP_STORE_WRITE 7
+#define WKV_OP_STORE_READ 8
+WKV_API wkv_status wkv_ssm_call(wkv_ssm_op op, const int64_t *args, int count);
+
 #ifdef __cplusplus
 }
 #endif

@@ -78,7 +78,13 @@ SSM_SIGNATURES = {
     "wkv_ssm_scan_forward_varlen": (_i, [_i] * 4 + [_vp, _i, _i] + _scan + [_vp, _i] + _seq_slots[:4] + [_vp, _sz, _vp, _vp]),
     "wkv_state_store_write": (_i, _store),
     "wkv_state_store_read": (_i, _store),
+    "wkv_ssm_call": (_i, [_i, ctypes.c_char_p, _i]),
 }
+
+# wkv_ssm_call's ops, in their order
+SSM_OPS = ("wkv_ssm_conv_forward", "wkv_ssm_conv_forward_varlen", "wkv_ssm_conv_backward", "wkv_ssm_scan_forward",
+           "wkv_ssm_scan_forward_train", "wkv_ssm_scan_forward_varlen", "wkv_ssm_scan_backward", "wkv_state_store_write",
+           "wkv_state_store_read")
 
 _lib = None
 

@@ -2,6 +2,10 @@
 // host-checkable problem is reported before any HIP call.
 #include "wkv_ssm.h"
 
+#include <limits>
+#include <type_traits>
+#include <utility>
+
 #include "api_common.hpp"
 #include "ssm.hpp"
 
@@ -226,6 +230,30 @@ wkv_status store(const char *fn, const void *data, const float *scale, int n_sto
   return WKV_OK;
 }
 
+// A parameter from its word; `fits` is cleared where the word is out of its range.
+template <class T>
+T from_word(int64_t w, bool &fits) {
+  if constexpr (std::is_pointer_v<T>) {
+    return reinterpret_cast<T>(static_cast<uintptr_t>(w));
+  } else {
+    if (sizeof(T) < sizeof w && (w < std::numeric_limits<T>::min() || w > std::numeric_limits<T>::max())) fits = false;
+    return static_cast<T>(w);
+  }
+}
+
+template <class... A, size_t... I>
+wkv_status call_words(const char *fn, wkv_status (*f)(A...), const int64_t *w, int count, std::index_sequence<I...>) {
+  REQUIRE(count == (int)sizeof...(A), "%s: takes %d arguments (got %d)", fn, (int)sizeof...(A), count);
+  bool fits = true;
+  const auto call = [&](A... a) { return fits ? f(a...) : fail(WKV_ERR_INVALID_ARG, "%s: an argument is out of its range", fn); };
+  return call(from_word<A>(w[I], fits)...);
+}
+
+template <class... A>
+wkv_status call_words(const char *fn, wkv_status (*f)(A...), const int64_t *w, int count) {
+  return call_words(fn, f, w, count, std::make_index_sequence<sizeof...(A)>{});
+}
+
 }  // namespace
 
 extern "C" {
@@ -433,6 +461,23 @@ wkv_status wkv_state_store_read(const void *data, const float *scale, int n_stor
   CHECK(store(fn, data, scale, n_store, format, states, n_state, row, store_rows, state_rows, count, dev_status, &p));
   if (count == 0) return ok();
   return launched(wkv::launch_store_read(p, static_cast<hipStream_t>(stream)), fn);
+}
+
+wkv_status wkv_ssm_call(wkv_ssm_op op, const int64_t *args, int count) {
+  const char *fn = "wkv_ssm_call";
+  REQUIRE(args, "%s: args must be non-NULL", fn);
+  switch (op) {
+    case WKV_OP_CONV_FORWARD: return call_words(fn, wkv_ssm_conv_forward, args, count);
+    case WKV_OP_CONV_FORWARD_VARLEN: return call_words(fn, wkv_ssm_conv_forward_varlen, args, count);
+    case WKV_OP_CONV_BACKWARD: return call_words(fn, wkv_ssm_conv_backward, args, count);
+    case WKV_OP_SCAN_FORWARD: return call_words(fn, wkv_ssm_scan_forward, args, count);
+    case WKV_OP_SCAN_FORWARD_TRAIN: return call_words(fn, wkv_ssm_scan_forward_train, args, count);
+    case WKV_OP_SCAN_FORWARD_VARLEN: return call_words(fn, wkv_ssm_scan_forward_varlen, args, count);
+    case WKV_OP_SCAN_BACKWARD: return call_words(fn, wkv_ssm_scan_backward, args, count);
+    case WKV_OP_STORE_WRITE: return call_words(fn, wkv_state_store_write, args, count);
+    case WKV_OP_STORE_READ: return call_words(fn, wkv_state_store_read, args, count);
+    default: return fail(WKV_ERR_INVALID_ARG, "%s: unknown op %d", fn, op);
+  }
 }
 
 }  // extern "C"

@@ -12,6 +12,8 @@ apart from a state updated in place.
 """
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import _native
@@ -23,6 +25,12 @@ __all__ = ["ssm_conv_forward", "ssm_conv_backward", "ssm_conv_forward_varlen", "
            "state_store_alloc", "state_store_write", "state_store_read"]
 
 _lib = _native.load()
+_call_words = _lib.wkv_ssm_call
+
+# A call's arguments travel as packed words: ctypes would spend 2 us on converting thirty of them one by one.
+(_CONV, _CONV_VARLEN, _CONV_BACKWARD, _SCAN, _SCAN_TRAIN, _SCAN_VARLEN, _SCAN_BACKWARD, _STORE_WRITE, _STORE_READ) = (
+    (op, struct.Struct(f"{len(_native.SSM_SIGNATURES[name][1])}q").pack, len(_native.SSM_SIGNATURES[name][1]))
+    for op, name in enumerate(_native.SSM_OPS))
 
 _CODES = {torch.bfloat16: _native.WKV_BF16, torch.float32: _native.WKV_F32}
 _ACTS = {None: _native.WKV_ACT_NONE, "none": _native.WKV_ACT_NONE, "silu": _native.WKV_ACT_SILU}
@@ -47,9 +55,9 @@ class _Call:
             raise ValueError(f"{name} must be a device tensor")
 
     def flat(self, t, name, shape, dtype=torch.float32):
-        """The address of a contiguous tensor of this shape and dtype; None for None."""
+        """The address of a contiguous tensor of this shape and dtype; 0 for None."""
         if t is None:
-            return None
+            return 0
         try:
             if t.shape == shape and t.dtype is dtype and t.get_device() == self.dev and t.is_contiguous():
                 return t.data_ptr()
@@ -123,16 +131,17 @@ def _row_step(t, name, lead):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _launch(dev, fn, *args):
+def _launch(dev, to, *args):
     """Calls the library with the current stream of the tensors' device, that device being current."""
+    op, pack, count = to
     if dev == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        status = _call_words(op, pack(*args, torch._C._cuda_getCurrentRawStream(dev)), count)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = _call_words(op, pack(*args, torch.cuda.current_stream(dev).cuda_stream), count)
     if status:
         check(status)
 
@@ -186,7 +195,7 @@ def ssm_conv_forward(x, weight, bias=None, state=None, state_map=None, *, activa
     W, par = _conv_params(call, weight, bias, activation)
     states, state_out = _dense_states(call, state, state_map, state_out, return_state, B, (W - 1, D))
     y, oc = call.output(y, out_dtype)
-    _launch(call.dev, _lib.wkv_ssm_conv_forward, B, T, D, W, *call.rows(x, "x", x.shape, 2), call.code, *par, y.data_ptr(), oc,
+    _launch(call.dev, _CONV, B, T, D, W, *call.rows(x, "x", x.shape, 2), call.code, *par, y.data_ptr(), oc,
             *states, call.status(dev_status))
     return y, state_out
 
@@ -213,7 +222,7 @@ def ssm_conv_backward(x, weight, bias, dy, state=None, state_map=None, *, activa
     d_first = call.empty((B, W - 1, D)) if return_d_state else None
     need = _lib.wkv_ssm_conv_backward_workspace(B, T, D, W)
     ws = call.empty((need // 4,))
-    _launch(call.dev, _lib.wkv_ssm_conv_backward, B, T, D, W, *call.rows(x, "x", x.shape, 2), call.code, *par,
+    _launch(call.dev, _CONV_BACKWARD, B, T, D, W, *call.rows(x, "x", x.shape, 2), call.code, *par,
             *call.rows(dy, "dy", x.shape, 2, any_dtype=True), _CODES[dy.dtype], si, mp, n_state, ds, _ptr(dx), _CODES[grad_dtype],
             _ptr(dw), _ptr(db), _ptr(d_first), _ptr(ws), need, call.status(dev_status))
     return dx, dw, db, d_first
@@ -231,7 +240,7 @@ def ssm_conv_forward_varlen(lengths, x, weight, bias, state, *, max_len, state_o
     W, par = _conv_params(call, weight, bias, activation)
     S, ln, states = _slot_states(call, lengths, state, state_map, state_out, (W - 1, D))
     y, oc = call.output(y, out_dtype)
-    _launch(call.dev, _lib.wkv_ssm_conv_forward_varlen, S, D, W, ln, int(max_len), total, *call.rows(x, "x", x.shape, 1), call.code,
+    _launch(call.dev, _CONV_VARLEN, S, D, W, ln, int(max_len), total, *call.rows(x, "x", x.shape, 1), call.code,
             *par, y.data_ptr(), oc, *states, call.status(dev_status))
     return y
 
@@ -249,7 +258,7 @@ def _scan_args(call, x, dt, A, B, C, D, z, dt_bias, dt_softplus):
     inner = (*shape[:k], G, N) if B.dim() == k + 2 else (*shape[:k], N)
     return width, N, G, (*call.rows(x, "x", shape, k), *call.rows(dt, "dt", shape, k), call.flat(A, "A", (width, N)),
                          *call.rows(B, "B", inner, k), *call.rows(C, "C", inner, k), call.code, call.flat(D, "D", (width,)),
-                         *(call.rows(z, "z", shape, k) if z is not None else (None, 0)),
+                         *(call.rows(z, "z", shape, k) if z is not None else (0, 0)),
                          call.flat(dt_bias, "dt_bias", (width,)), 1 if dt_softplus else 0)
 
 
@@ -276,7 +285,7 @@ def ssm_scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, s
     states, state_out = _dense_states(call, state, state_map, state_out, return_state, rows, (width, N))
     y, oc = call.output(y, out_dtype)
     ws, ws_bytes = _workspace(call, rows, T, rows * T, width, N, G)
-    _launch(call.dev, _lib.wkv_ssm_scan_forward, rows, T, width, N, G, *args, y.data_ptr(), oc, *states, _ptr(ws), ws_bytes,
+    _launch(call.dev, _SCAN, rows, T, width, N, G, *args, y.data_ptr(), oc, *states, _ptr(ws), ws_bytes,
             call.status(dev_status))
     return y, state_out
 
@@ -301,8 +310,8 @@ def ssm_scan_forward_train(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=N
     if chunk_states is None:
         chunk_states = call.empty(saved)
     ws, ws_bytes = _workspace(call, rows, T, rows * T, width, N, G)
-    _launch(call.dev, _lib.wkv_ssm_scan_forward_train, rows, T, width, N, G, *args, y.data_ptr(), oc, *states,
-            call.flat(chunk_states, "chunk_states", saved) or None, _ptr(ws), ws_bytes, call.status(dev_status))
+    _launch(call.dev, _SCAN_TRAIN, rows, T, width, N, G, *args, y.data_ptr(), oc, *states,
+            call.flat(chunk_states, "chunk_states", saved), _ptr(ws), ws_bytes, call.status(dev_status))
     return y, state_out, chunk_states
 
 
@@ -326,7 +335,7 @@ def ssm_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, state=No
     if grad_dtype not in _CODES:
         raise TypeError(f"unsupported gradient dtype {grad_dtype} (bfloat16 or float32)")
     dya = call.rows(dy, "dy", x.shape, 2, any_dtype=True)
-    chunks = call.flat(chunk_states, "chunk_states", (rows, _chunks(T), width, N)) or None
+    chunks = call.flat(chunk_states, "chunk_states", (rows, _chunks(T), width, N))
     ds = call.flat(d_state, "d_state", (rows, width, N))
     dx, ddt = call.like(x, grad_dtype), call.like(dt, grad_dtype)
     dB, dC = call.like(B, grad_dtype), call.like(C, grad_dtype)
@@ -335,9 +344,9 @@ def ssm_scan_backward(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, state=No
     dD = call.like(D, torch.float32) if D is not None else None
     db = call.like(dt_bias, torch.float32) if dt_bias is not None else None
     d_first = call.empty((rows, width, N)) if return_d_state else None
-    need = _lib.wkv_ssm_scan_backward_workspace(rows, T, width, N, G, int(chunks is not None or _chunks(T) == 0))
+    need = _lib.wkv_ssm_scan_backward_workspace(rows, T, width, N, G, int(chunks != 0 or _chunks(T) == 0))
     ws = call.empty((need // 4,))
-    _launch(call.dev, _lib.wkv_ssm_scan_backward, rows, T, width, N, G, *args, *dya, _CODES[dy.dtype], si, mp, n_state, chunks, ds,
+    _launch(call.dev, _SCAN_BACKWARD, rows, T, width, N, G, *args, *dya, _CODES[dy.dtype], si, mp, n_state, chunks, ds,
             _ptr(dx), _ptr(ddt), _ptr(dB), _ptr(dC), _ptr(dz), _CODES[grad_dtype], _ptr(dA), _ptr(dD), _ptr(db),
             _ptr(d_first), _ptr(ws), need, call.status(dev_status))
     return dx, ddt, dA, dB, dC, dD, dz, db, d_first
@@ -356,7 +365,7 @@ def ssm_scan_forward_varlen(lengths, x, dt, A, B, C, state, *, max_len, D=None, 
     S, ln, states = _slot_states(call, lengths, state, state_map, state_out, (width, N))
     y, oc = call.output(y, out_dtype)
     ws, ws_bytes = _workspace(call, S, int(max_len), total, width, N, G)
-    _launch(call.dev, _lib.wkv_ssm_scan_forward_varlen, S, width, N, G, ln, int(max_len), total, *args, y.data_ptr(), oc,
+    _launch(call.dev, _SCAN_VARLEN, S, width, N, G, ln, int(max_len), total, *args, y.data_ptr(), oc,
             *states, _ptr(ws), ws_bytes, call.status(dev_status))
     return y
 
@@ -397,11 +406,11 @@ def state_store_write(data, scale, states, store_rows=None, state_rows=None, *, 
     Item i stores ``states[state_rows[i]]`` as row ``store_rows[i]`` (int32 device tensors; None: i).
     Groups of 64 consecutive values share the scale max|v| / 127 (int8) or / 448 (e4m3).
     """
-    _store_call(_lib.wkv_state_store_write, data, scale, states, store_rows, state_rows, dev_status)
+    _store_call(_STORE_WRITE, data, scale, states, store_rows, state_rows, dev_status)
 
 
 def state_store_read(data, scale, states, store_rows=None, state_rows=None, *, dev_status=None):
     """Reads rows of the 8-bit store back into ``states`` (see :func:`state_store_write`); one stored row may
     be read into many state rows.  Returns ``states``."""
-    _store_call(_lib.wkv_state_store_read, data, scale, states, store_rows, state_rows, dev_status)
+    _store_call(_STORE_READ, data, scale, states, store_rows, state_rows, dev_status)
     return states

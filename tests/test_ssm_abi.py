@@ -177,3 +177,32 @@ def test_forward_train_needs_room_for_its_states(lib):
     assert lib.wkv_ssm_scan_forward_train(*args(17, None)) == E and b"chunk_states" in lib.wkv_last_error()
     assert lib.wkv_ssm_scan_forward_train(*args(17, 0x10008)) == E
     assert lib.wkv_ssm_scan_forward_train(*args(0, None)) == OK
+
+
+def test_calls_by_words(lib):
+    import struct
+    text = open(os.path.join(ROOT, "include", "wkv_ssm.h")).read()
+    ops = {int(n): "wkv_" + ("state_" if name.startswith("STORE") else "ssm_") + name.lower()
+           for name, n in re.findall(r"#define WKV_OP_(\w+) (\d+)", text)}
+    assert [ops[i] for i in range(len(ops))] == list(nat.SSM_OPS)
+    for op, name in enumerate(nat.SSM_OPS):
+        n = len(nat.SSM_SIGNATURES[name][1])
+        zeros = struct.pack(f"{n}q", *[0] * n)
+        for count in (n - 1, n + 1, -1):
+            assert lib.wkv_ssm_call(op, zeros, count) == E and b"arguments" in lib.wkv_last_error()
+        # a call of zeros is refused, by the same words either way
+        want = lib[name]
+        want.restype, want.argtypes = nat.SSM_SIGNATURES[name]
+        assert lib.wkv_ssm_call(op, zeros, n) == want(*[0] * n) != OK, name
+        said = lib.wkv_last_error()
+        want(*[0] * n)
+        assert said == lib.wkv_last_error() and name.encode() in said
+        for big in (1 << 31, -(1 << 31) - 1):
+            first = next(i for i, t in enumerate(nat.SSM_SIGNATURES[name][1]) if t is nat.SSM_SIGNATURES["wkv_ssm_conv_forward"][1][0])
+            words = [0] * n
+            words[first] = big
+            assert lib.wkv_ssm_call(op, struct.pack(f"{n}q", *words), n) == E and b"range" in lib.wkv_last_error()
+    assert lib.wkv_ssm_call(len(nat.SSM_OPS), zeros, 1) == E and lib.wkv_ssm_call(-1, zeros, 1) == E
+    assert lib.wkv_ssm_call(0, None, 19) == E
+    words = [0, 64, 4, P, 8, 16, P, 64, 1, P, P, 1, 2 * P, 0, P, P, 0, 2, 0, 0]  # no slots: nothing to do
+    assert lib.wkv_ssm_call(nat.SSM_OPS.index("wkv_ssm_conv_forward_varlen"), struct.pack("20q", *words), 20) == OK
