@@ -100,10 +100,10 @@ class _Call:
 
     def like(self, t, dtype):
         """An empty contiguous tensor of t's shape."""
-        return torch.empty_like(t) if t.dtype is dtype and t.is_contiguous() else torch.empty(t.shape, dtype=dtype, device=t.device)
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
     def empty(self, shape, dtype=torch.float32):
-        return torch.empty(shape, dtype=dtype, device=self.ref.device)
+        return self.ref.new_empty(shape, dtype=dtype)
 
     def status(self, dev_status):
         return self.flat(dev_status, "dev_status", (1,), torch.int32)
