@@ -696,3 +696,49 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i, (y, last) in enumerate(got):
         assert torch.equal(y, alone[i % 2][0]) and torch.equal(last, alone[i % 2][1])
+
+
+# ------------------------------------------------------------------------------------------- past 32 bits
+
+def test_token_offsets_past_32_bits():
+    """More than 2^31 elements of a token array: silence up to the last tokens, which must be those of a call of their own."""
+    D, tail = 4096, 70
+    T = (1 << 31) // D + 33 + tail
+    x = torch.zeros(1, T, D, dtype=BF16, device="cuda")
+    x[:, -tail:] = gpu(draw(90, 1, tail, D, dtype=BF16))
+    weight = gpu(draw(91, D, 4))
+    y, last = wkv.ssm_conv_forward(x, weight, activation="silu", out_dtype=BF16)
+    want, end = wkv.ssm_conv_forward(x[:, -tail:].contiguous(), weight, activation="silu", out_dtype=BF16)
+    assert torch.equal(y[:, -tail:], want) and torch.equal(last, end) and not y[:, :-tail].any()
+    bc = gpu(draw(92, 1, T, 4, dtype=BF16))
+    A = -gpu(draw(93, D, 4)).abs()
+    y, last = wkv.ssm_scan_forward(x, x, A, bc, bc, out_dtype=BF16, y=y)
+    near = [t[:, -tail:].contiguous() for t in (x, bc)]
+    want, end = wkv.ssm_scan_forward(near[0], near[0], A, near[1], near[1], out_dtype=BF16)
+    # a state of zeros stays one over any segment: the same operations on the same values
+    assert torch.equal(y[:, -tail:], want) and torch.equal(last, end) and not y[:, :-tail].any()
+
+
+def test_state_offsets_past_32_bits():
+    """State tables of more than 2^31 values: steps, and the store's rows, at their ends."""
+    D, N = 2048, 32
+    rows = (1 << 31) // (D * N) + 5
+    c = scan_case(0, 0, D, N, 0, BF16, seed=94, lead=(2,), n_state=2)
+    table = torch.zeros(rows, D, N, device="cuda")
+    table[rows - 2:] = gpu(c["state"])
+    few = gpu(c["state"])
+    ln, at = gpu(torch.tensor([1, 1], dtype=torch.int32)), gpu(torch.tensor([rows - 1, rows - 2], dtype=torch.int32))
+    args = [gpu(c[k]) for k in ("x", "dt", "A", "B", "C")]
+    got = wkv.ssm_scan_forward_varlen(ln, *args, table, max_len=1, state_map=at)
+    want = wkv.ssm_scan_forward_varlen(ln, *args, few, max_len=1, state_map=gpu(torch.tensor([1, 0], dtype=torch.int32)))
+    assert torch.equal(got, want) and torch.equal(table[rows - 2:], few) and not table[rows - 4:rows - 2].any()
+    data, scale = wkv.state_store_alloc(rows, D * N)
+    wkv.state_store_write(data, scale, table, store_rows=at, state_rows=at)
+    small, small_scale = wkv.state_store_alloc(2, D * N)
+    wkv.state_store_write(small, small_scale, few)
+    assert torch.equal(data[rows - 2:], small) and torch.equal(scale[rows - 2:], small_scale) and not data[rows - 4:rows - 2].any()
+    back = torch.ones(2, D, N, device="cuda")
+    wkv.state_store_read(data, scale, back, store_rows=at, state_rows=gpu(torch.tensor([1, 0], dtype=torch.int32)))
+    want = torch.empty_like(back)
+    wkv.state_store_read(small, small_scale, want)
+    assert torch.equal(back, want)
