@@ -466,8 +466,10 @@ hipError_t by_states(const ScanSsmParams &p, hipStream_t s) {
 // Segments of a call, by a model of its time in tokens of one workgroup walking alone.  A compute
 // unit that has k workgroups takes `shared` k times as long for a token of each (two at once overlap a
 // little; measured 0.88 forward, and 1 backward, where one fills the unit); the carry pass costs the
-// share `carry` of the main one, and a workgroup's start as well as a launch as much as `start` tokens.  groups: the workgroups of
-// one segment of all rows.
+// share `carry` of the main one, and a workgroup's start as well as a launch as much as `start` tokens.
+// groups: the workgroups of one segment of all rows.  Measured around its choices: [1, 32765, 1536] 327 us
+// in the 21 that it takes, 388 in 10, 420 in 16, 318 in 32; [8, 4096, 2048] 280 uncut, 342 in two; 48
+// mixed slots 67 uncut, 105 in two; training [2, 777, 1030] 116, 199 with its backward pass uncut.
 int best_segments(long groups, int T, int step, double shared, double carry, int start, int *seg_len) {
   *seg_len = T > 0 ? T : 1;
   if (T <= kScanSplit || groups < 1) return 1;
